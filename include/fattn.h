@@ -309,6 +309,170 @@ int attn_decode_auto_splits(int B, int H, int Lk, int d);
 size_t attn_decode_workspace_bytes(int B, int H, int Lk, int d, int num_splits);
 
 /*
+ * The paged 8-bit KV cache.  Four entry points serve a model whose keys and
+ * values are held as e4m3 codes in fixed-size pages ("算子与编译器：
+ * FlashAttention 与长上下文" §5, paged KV cache), one scale per page and head:
+ *
+ *   attn_paged_plan        block tables and slot maps from request lengths
+ *   attn_append_paged_fp8  new K/V rows quantized into the pages
+ *   attn_decode_paged_fp8  one new query per sequence over the cache
+ *   attn_fwd_paged_fp8     several new queries per sequence over the cache
+ *
+ * The cache:
+ *   k_pages, v_pages    device, e4m3 codes [num_pages, page_size, Hkv, d]
+ *                       (token-major pages, as attn_decode_paged); d 64 or 128,
+ *                       16-byte aligned; num_pages * page_size <= 2^40
+ *   k_scales, v_scales  device, fp32 [num_pages, Hkv], finite and > 0: code c of
+ *                       page p and head h stands for e4m3(c) * scales[p, h]
+ *   page_size           a power of two >= 16
+ *   block_table         device, int32 [B, max_pages]: logical page i of sequence
+ *                       b is physical page block_table[b*max_pages + i]; the
+ *                       attention calls clamp indices into [0, num_pages)
+ *   slot                page * page_size + offset of a token's row, 64 bits
+ * Heads are shared: Hq query heads use Hkv key/value heads, query head j reads
+ * head j / (Hq / Hkv); Hkv divides Hq and Hq / Hkv <= 128.
+ */
+
+/*
+ * attn_paged_plan -- where the new tokens of a batch go.  Sequence b holds
+ * seqlens_k[b] tokens and receives seqlens_new[b]; its pages below
+ * ceil(seqlens_k[b] / page_size) are in the block table, the further ones it
+ * needs are taken from the free list in the order of the sequences.
+ *
+ *   seqlens_k    device, int32 [B]; negative counts as 0
+ *   seqlens_new  device, int32 [B]; negative counts as 0
+ *   free_pages   device, int32 [num_free], physical pages not in use (may be
+ *                NULL when num_free = 0); only read
+ *   block_table  device, int32 [B, max_pages]: the entries of the pages taken
+ *                are written, all others are left as they were
+ *   slot_map     device, int64 [max_tokens] (written): the slot of every token
+ *                of the packed batch, sequence after sequence; -1 for the
+ *                places behind the last token, and for a token that has no page
+ *                (beyond the free list, beyond max_pages, or in a page whose
+ *                table entry is negative)
+ *   cu_seqlens   device, int32 [B + 1] (written): prefix sums of seqlens_new, the
+ *                cu_seqlens_q of attn_fwd_paged_fp8
+ *   seqlens_out  device, int32 [B] (written): seqlens_k + seqlens_new; not
+ *                overlapping the inputs
+ *   counts       device, int32 [2] (written): tokens of the batch, and pages it
+ *                needs.  counts[0] > max_tokens or counts[1] > num_free says that
+ *                some tokens have no slot; the next free list is
+ *                free_pages + counts[1].
+ * B <= 16384.  One kernel; sums beyond 2^31 - 1 are written as 2^31 - 1.
+ * Everything is read on the device, so a captured graph takes new lengths (up
+ * to max_tokens tokens) on every replay.
+ */
+int attn_paged_plan(const int* seqlens_k, const int* seqlens_new, int B,
+                    const int* free_pages, int num_free,
+                    int* block_table, int max_pages, int page_size,
+                    long long* slot_map, int max_tokens,
+                    int* cu_seqlens, int* seqlens_out, int* counts, void* stream);
+
+/*
+ * attn_append_paged_fp8 -- quantize new K and V rows into the cache.
+ *
+ *   k, v        device, bf16: row of token t and head h at k + t*k_stride + h*d,
+ *               d contiguous elements (views of a fused projection fit); 16-byte
+ *               aligned, strides in elements, multiples of 8, >= H*d
+ *   slot_map    device, int64 [num_tokens]: token t goes to row
+ *               slot_map[t] % page_size of page slot_map[t] / page_size; a slot
+ *               outside [0, num_pages*page_size) means that t is not stored.
+ *               The tokens of one page stand together in the batch, on rising
+ *               slots that leave no gap (the maps of attn_paged_plan do).  A slot
+ *               that such a stretch names twice keeps the later token.  A page
+ *               that is named by two separate stretches of one call gets an
+ *               unspecified content.
+ *   k_pages, v_pages, k_scales, v_scales: the cache (read and written), H = Hkv
+ *
+ * For every page and head that receives rows, with amax the largest finite
+ * |x| of the new rows and r the offset of the first of them:
+ *   s_new = 2^max(e, -60), e the smallest integer with amax <= 448 * 2^e
+ *   s     = max(s_old, s_new) if r > 0 (the page's rows below r are kept), else s_new
+ *   rows below r, if s > s_old:  code = e4m3(e4m3(code) * (s_old * (1/s)))
+ *   the new rows:                code = e4m3(x * (1/s))
+ * e4m3() rounds to nearest, ties to even; products and the reciprocal are one
+ * fp32 operation each.  With power-of-two scales (all that this function
+ * writes) they are exact, so a code rounds once when it is written, by at most
+ * 2^-4 of the value (2^-10 of the scale below 2^-6 of it), and again only where
+ * a growing scale moves it below 2^-6, by at most 2^-10 of the new scale.
+ * An infinity or a NaN is stored as e4m3's NaN and takes no part in amax.
+ * Rows of the page behind the new ones are left as they were (their codes are
+ * stale: the attention calls never use rows behind seqlens_k).
+ */
+int attn_append_paged_fp8(const void* k, const void* v, long long k_stride, long long v_stride,
+                          const long long* slot_map, int num_tokens,
+                          void* k_pages, void* v_pages, float* k_scales, float* v_scales,
+                          int num_pages, int page_size, int H, int d, void* stream);
+
+/*
+ * attn_decode_paged_fp8 -- attn_decode_paged over the 8-bit cache: one new
+ * query per sequence, already counted in seqlens_k.
+ *
+ *   q            device, bf16 [B,Hq,1,d], 16-byte aligned
+ *   o, lse       device, bf16 [B,Hq,1,d] / fp32 [B,Hq] (written; lse nullable)
+ *   seqlens_k    device, int32 [B], required, clamped to [0, max_pages*page_size].
+ *                A sequence of length 0 gets O = 0 and LSE = -inf.
+ *   window_left  keys [seqlens_k[b] - 1 - window_left, seqlens_k[b]) are attended
+ *                (negative: all); pages before the window are not read
+ *   num_splits   splits of a sequence's attended keys at most (evenly, by the
+ *                sequence's own length, at least 64 keys to a split), or 0 for
+ *                attn_decode_paged_fp8_auto_splits(B, Hq, Hkv, max_pages*page_size, d)
+ *   workspace    device scratch of attn_decode_workspace_bytes(B, Hq, Lk, d, S)
+ *                bytes for S splits, 16-byte aligned; not needed (may be NULL)
+ *                when S = 1; contents ignored on entry, unspecified on return
+ * Codes enter the products exactly (as f16), a query row is scaled by a power of
+ * two before it is rounded to f16 (exact down to 2^-14 of the row's largest
+ * element), probabilities are rounded to f16 (2^-11 of each), sums and
+ * statistics are fp32, O is rounded to bf16 once.  Key rows outside the attended
+ * range have no effect, whatever their codes are (NaN included).  The V scales
+ * of one sequence may differ by up to 2^80; one below 2^-100 counts as 2^-100.
+ */
+int attn_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
+                          const float* k_scales, const float* v_scales,
+                          const int* block_table, int max_pages, int page_size, int num_pages,
+                          void* o, float* lse, const int* seqlens_k, int B, int Hq, int Hkv, int d,
+                          float scale, int window_left, int num_splits,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* Split count attn_decode_paged_fp8 uses for num_splits = 0 (host only). */
+int attn_decode_paged_fp8_auto_splits(int B, int Hq, int Hkv, int Lk, int d);
+
+/*
+ * attn_fwd_paged_fp8 -- packed prefill over the 8-bit cache: the new tokens of
+ * every sequence (a chunk of a prompt, drafted tokens to verify, one decoded
+ * token) attend to the sequence's cached keys, their own included, which are in
+ * the cache already.
+ *
+ *   q, o          device, bf16 [total_q, Hq, d], token-major, 16-byte aligned
+ *   lse           device, fp32 [Hq, total_q], or NULL
+ *   cu_seqlens_q  device, int32 [B + 1], non-decreasing: sequence b owns query
+ *                 tokens [cu_seqlens_q[b], cu_seqlens_q[b+1]); rows behind
+ *                 cu_seqlens_q[B] are not written
+ *   max_seqlen_q  at least every sequence's query length (query rows beyond it
+ *                 are not computed)
+ *   seqlens_k     device, int32 [B]: keys of the sequence, the new ones included
+ *   causal, window_left, window_right: the mask of attn_fwd per sequence
+ *                 (bottom-right aligned: the last query sits at the last key)
+ *   workspace     device scratch of attn_fwd_paged_fp8_workspace_bytes bytes,
+ *                 16-byte aligned (may be NULL when that is 0)
+ * Offsets and lengths are clamped so that no access leaves the tensors.
+ * Precision and key rows outside the mask as attn_decode_paged_fp8; a row
+ * with no allowed key gets O = 0 and LSE = -inf.
+ */
+int attn_fwd_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
+                       const float* k_scales, const float* v_scales,
+                       const int* block_table, int max_pages, int page_size, int num_pages,
+                       void* o, float* lse, const int* seqlens_k, const int* cu_seqlens_q,
+                       int B, int total_q, int max_seqlen_q, int Hq, int Hkv, int d, float scale,
+                       int causal, int window_left, int window_right,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace attn_fwd_paged_fp8 needs for these sizes, Lk =
+ * max_pages * page_size (host only; 0 on invalid sizes too). */
+size_t attn_fwd_paged_fp8_workspace_bytes(int B, int total_q, int max_seqlen_q,
+                                          int Hq, int Hkv, int Lk, int d);
+
+/*
  * attn_count_blocks -- host-only block accounting of the scheduler (§5.4):
  * for block_q x block_k tiles of one head's Lq x Lk score matrix,
  *   visited = tiles holding at least one allowed pair (exactly the tiles the

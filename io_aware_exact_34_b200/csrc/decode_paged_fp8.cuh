@@ -1,0 +1,659 @@
+// decode_paged_fp8.cuh -- attention of few query rows per sequence over a paged
+// 8-bit cache: split-KV decode, and short runs of new tokens (verification).
+//
+// For a kv head h and its group of g = Hq / Hkv query heads, the rows of one
+// sequence are (new token i, group head j) -> row i*g + j.  With block scales
+// ks, vs (one per page and kv head) and codes K, V,
+//   x = scale * ks * (q . K_code),   p = 2^(x log2e),   l = sum p,
+//   o = (sum p * vs * V_code) / l.
+// The scale of V goes into the exponent, y = x log2e + log2 vs, and the
+// running reference my follows y, not x: p' = 2^(y - my + 7) <= 2^15 goes into
+// the P V product as f16, l sums p' / vs in fp32, and o = acc / l,
+// lse = my + log2 l - 7.  So one exponential serves both sums, and the largest
+// term of the numerator always sits in f16's normal range, whatever the pages'
+// scales are.  The reference moves only when some y passes it by more than 8
+// (as in the prefill kernels), which keeps reductions out of the loop.
+//
+// Products run on mma.sync m16n8k16 with f16 operands and fp32 accumulation:
+// e4m3 is a subset of f16, so codes convert exactly; a query row is scaled by
+// a power of two to a largest magnitude in [1, 2) before it becomes f16 (11
+// bits against bf16's 8, so nothing is lost down to 2^-14 of the row's
+// largest element); P is rounded to f16 (relative 2^-11).  The key rows are the
+// M operand and 8 query rows the N operand: S^T = K Q^T and O^T = V^T P^T waste
+// nothing at 8 rows a group, where Q as the M operand would pay for 16.
+// A decode step reads 2*d bytes per key and kv head and is bound by that;
+// tcgen05 would add nothing here but the round trip through tensor memory.
+//
+// Loads: a warp takes 16 keys a step (16 divides every page, so one page and
+// one pair of scales per step) through a ring of cp.async stages in shared
+// memory.  Every lane copies exactly the bytes it reads back itself, so the
+// ring needs no barrier between lanes (only the two scales are shared by the
+// warp), and the fragments need no transposition:
+//   K: lane (r = lane/4, c = lane%4) holds 16 bytes of rows r and r + 8 per
+//      64-byte half; the product's k index runs over d in that order, for Q too;
+//   V: the lane holds D/8 bytes of rows 2c, 2c+1, 2c+8, 2c+9; PRMT pairs the
+//      bytes of two rows, and a pair converts to one A register of V^T;
+//   P: S^T's accumulator transposes to the B operand of O^T by movmatrix.
+// Rows outside the keys that some row of the tile may see are filled with
+// zeros, so stale codes there (NaN too) never reach a product.
+//
+// Split: a sequence's key blocks are divided evenly over at most S CTAs of 4
+// warps (by the sequence's own length, not the table's width); the merge
+// kernel combines the splits' (o, lse) and starts by programmatic launch.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math_constants.h>
+
+#include "dev_prims.cuh"
+#include "paged_fp8_append.cuh"
+
+namespace fattn {
+
+constexpr int DP8_WARPS = 4;
+constexpr int DP8_BLOCK = 16;       // keys per warp step
+constexpr int DP8_MIN_BLOCKS = 4;   // key blocks of the smallest split: one per warp
+constexpr int kDp8TargetCtas = 4096;  // CTAs the automatic split aims at
+constexpr float kDp8Shift = 7.f;    // p' = 2^(y - my + 7)
+constexpr float kDp8Slack = 8.f;
+constexpr float kMinValueScale = 7.888609052210118e-31f;  // 2^-100: smaller V scales count as this
+
+struct PagedFp8Params {
+    const __nv_bfloat16* q;     // rows (token, query head) of d elements
+    const uint8_t *k, *v;       // [num_pages, page_size, Hkv, d]
+    const float *ks, *vs;       // [num_pages, Hkv]
+    const int* block_table;     // [B, max_pages]
+    const int* seqlens_k;       // [B]
+    const int* cu_q;            // [B + 1], or null: one token per sequence, token b
+    __nv_bfloat16* o;
+    float* lse;                 // or null
+    float *ws_o, *ws_lse;       // partials [row][split][d], [row][split]
+    long long lse_tok, lse_head;  // strides of lse
+    int B, Hq, Hkv, g, total_q, max_q;
+    int max_pages, page_shift, num_pages;
+    int S, row_tiles;
+    int causal, window_left, window_right;
+    float scale_log2;
+};
+
+// One sequence: first token, tokens, keys.
+struct SeqSpan {
+    int q0, n;
+    long long len;
+};
+
+__device__ __forceinline__ SeqSpan seq_span(const PagedFp8Params& p, int b) {
+    SeqSpan s;
+    if (p.cu_q != nullptr) {
+        auto clampi = [](int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); };
+        s.q0 = clampi(__ldg(p.cu_q + b), 0, p.total_q);
+        s.n = clampi(__ldg(p.cu_q + b + 1), s.q0, p.total_q) - s.q0;
+    } else {
+        s.q0 = b;
+        s.n = 1;
+    }
+    const long long cap = static_cast<long long>(p.max_pages) << p.page_shift;
+    const long long len = __ldg(p.seqlens_k + b);
+    s.len = len < 0 ? 0 : (len > cap ? cap : len);
+    return s;
+}
+
+// Keys [lo, hi) that the token i of the sequence may see.
+__device__ __forceinline__ void key_range(const PagedFp8Params& p, const SeqSpan& s, long long i, long long* lo, long long* hi) {
+    const long long pos = i + s.len - s.n;
+    long long h = s.len, l = 0;
+    if (p.causal && pos + 1 < h) h = pos + 1;
+    if (!p.causal && p.window_right >= 0 && pos + p.window_right + 1 < h) h = pos + p.window_right + 1;
+    if (p.window_left >= 0 && pos - p.window_left > 0) l = pos - p.window_left;
+    *lo = l;
+    *hi = h > l ? h : l;
+}
+
+// The key blocks of the rows' union and this split's share.
+struct SplitSpan {
+    long long k_lo, k_hi;   // union of the rows' keys
+    long long first, last;  // blocks of this split
+    int active;             // splits that hold blocks
+};
+
+__device__ __forceinline__ SplitSpan split_span(const PagedFp8Params& p, const SeqSpan& s, long long tok_lo, long long tok_hi, int split) {
+    SplitSpan r;
+    long long lo0, hi0, lo1, hi1;
+    key_range(p, s, tok_lo, &lo0, &hi0);
+    key_range(p, s, tok_hi, &lo1, &hi1);
+    r.k_lo = lo0;
+    r.k_hi = hi1;
+    r.first = r.last = 0;
+    r.active = 0;
+    if (r.k_hi <= r.k_lo) return r;
+    const long long b0 = r.k_lo / DP8_BLOCK, b1 = (r.k_hi + DP8_BLOCK - 1) / DP8_BLOCK;
+    long long per = (b1 - b0 + p.S - 1) / p.S;
+    per = (per + DP8_MIN_BLOCKS - 1) / DP8_MIN_BLOCKS * DP8_MIN_BLOCKS;
+    r.active = static_cast<int>((b1 - b0 + per - 1) / per);
+    r.first = b0 + split * per;
+    r.last = r.first + per < b1 ? r.first + per : b1;
+    return r;
+}
+
+template <int D>
+struct Dp8Traits {
+    static constexpr int STAGES = 4;
+    static constexpr int VB = D / 8;                        // bytes of a V row per lane
+    static constexpr int KV_BYTES = 2 * DP8_BLOCK * D;      // one step of one warp
+    static constexpr int WARP_BYTES = STAGES * KV_BYTES;
+    static constexpr int RING_BYTES = DP8_WARPS * WARP_BYTES;
+    static constexpr int SCALE_BYTES = DP8_WARPS * STAGES * 8;
+    static constexpr int SMEM_BYTES = RING_BYTES + SCALE_BYTES;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds_u4(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+
+__device__ __forceinline__ uint2 lds_u2(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+
+__device__ __forceinline__ float2 lds_f2(uint32_t a) {
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+    return v;
+}
+
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float fast_log2(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// True if one of the four bytes is e4m3's NaN (0x7F with either sign).
+__device__ __forceinline__ bool has_nan4(uint32_t w) { return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0; }
+
+// The power of two 2^-e and e for a row's largest magnitude, so that the row
+// times 2^-e has its largest element in [1, 2).
+__device__ __forceinline__ int row_exponent(float amax) {
+    int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+    return e < -100 ? -100 : (e > 126 ? 126 : e);
+}
+
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// NT tiles of 8 query rows per CTA.  kMasked: rows of the tile may see
+// different keys (more than one token per sequence).
+template <int D, int NT, bool kMasked>
+__global__ void __launch_bounds__(32 * DP8_WARPS) decode_paged_fp8_kernel(const PagedFp8Params p) {
+    using T = Dp8Traits<D>;
+    constexpr int ROWS = 8 * NT;
+    constexpr int HALVES = D / 64;
+    constexpr int MT = D / 16;  // 16-row tiles of O^T
+    extern __shared__ __align__(16) uint8_t dp8_smem[];
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r8 = lane >> 2, c4 = lane & 3;
+
+    // CTA = ((sequence, split), kv head, row tile), row tiles fastest
+    unsigned int x = blockIdx.x;
+    const int rt = x % p.row_tiles;
+    x /= p.row_tiles;
+    const int h = x % p.Hkv;
+    x /= p.Hkv;
+    const int split = x % p.S;
+    const int b = x / p.S;
+    const SeqSpan sq = seq_span(p, b);
+    const int n_tok = sq.n < p.max_q ? sq.n : p.max_q;
+    const int row0 = rt * ROWS, rows = n_tok * p.g - row0 < ROWS ? n_tok * p.g - row0 : ROWS;  // valid rows of the tile
+    if (rows <= 0) return;
+    const SplitSpan sp = split_span(p, sq, row0 / p.g, (row0 + rows - 1) / p.g, split);
+    if (split > 0 && split >= sp.active) return;
+
+    // element offset of a row in q and o, and its place in lse
+    auto row_q = [&](int r) -> long long {
+        const int i = (row0 + r) / p.g, j = (row0 + r) % p.g;
+        return ((static_cast<long long>(sq.q0) + i) * p.Hq + static_cast<long long>(h) * p.g + j) * D;
+    };
+    auto row_lse = [&](int r) -> long long {
+        const int i = (row0 + r) / p.g, j = (row0 + r) % p.g;
+        return (static_cast<long long>(sq.q0) + i) * p.lse_tok + (static_cast<long long>(h) * p.g + j) * p.lse_head;
+    };
+
+    const uint32_t ring = smem_addr(dp8_smem) + warp * T::WARP_BYTES;
+    const uint32_t sring = smem_addr(dp8_smem) + T::RING_BYTES + warp * T::STAGES * 8;
+    const long long nblk = sp.last - sp.first;
+    const int nsteps = sp.active == 0 ? 0 : static_cast<int>((nblk - warp + DP8_WARPS - 1) / DP8_WARPS);
+    const int shift = p.page_shift;
+    const long long head_row = static_cast<long long>(p.Hkv) * D;  // bytes between a head's rows
+    const int* table = p.block_table + static_cast<long long>(b) * p.max_pages;
+
+    int table_lane = 0;  // lane i: the page of step 32*(issued/32) + i
+    auto issue = [&](int i) {
+        if ((i & 31) == 0) {
+            const long long blk = sp.first + static_cast<long long>(i + lane) * DP8_WARPS + warp;
+            if (blk < sp.last) {
+                const int pg = __ldg(table + ((blk * DP8_BLOCK) >> shift));
+                table_lane = pg < 0 ? 0 : (pg >= p.num_pages ? p.num_pages - 1 : pg);
+            }
+        }
+        if (i < nsteps) {
+            const long long key0 = (sp.first + static_cast<long long>(i) * DP8_WARPS + warp) * DP8_BLOCK;
+            const long long page = __shfl_sync(0xffffffffu, table_lane, i & 31);
+            const long long row = (page << shift) + (key0 & ((1LL << shift) - 1));
+            const long long at = (row * p.Hkv + h) * D;
+            const uint32_t slot = ring + (i % T::STAGES) * T::KV_BYTES;
+            auto there = [&](int r) { return key0 + r >= sp.k_lo && key0 + r < sp.k_hi; };
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = r8 + 8 * e;
+                const uint8_t* src = p.k + at + r * head_row + c4 * 16;
+#pragma unroll
+                for (int hh = 0; hh < HALVES; ++hh)
+                    cp_async16(slot + ((e * HALVES + hh) * 32 + lane) * 16, src + hh * 64, there(r) ? 16 : 0);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = 2 * c4 + (e & 1) + 8 * (e >> 1);
+                const uint8_t* src = p.v + at + r * head_row + r8 * T::VB;
+                const uint32_t dst = slot + DP8_BLOCK * D + (e * 32 + lane) * T::VB;
+                if constexpr (D == 128) cp_async16(dst, src, there(r) ? 16 : 0);
+                else cp_async8(dst, src, there(r) ? 8 : 0);
+            }
+            const uint32_t sslot = sring + (i % T::STAGES) * 8;
+            if (lane < 2) cp_async4(sslot + 4 * lane, (lane == 0 ? p.ks : p.vs) + page * p.Hkv + h);
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < T::STAGES - 1; ++i) issue(i);
+
+    // Q^T fragments: column r8 of tile nt, d in the order of the K fragments
+    uint32_t qf[NT][HALVES][4][2];
+    float cq[NT][2];  // scale * log2e * 2^e of the rows 2*c4, 2*c4 + 1
+    [[maybe_unused]] int klo[NT][2], khi[NT][2];  // keys of those rows, relative to the union's first key
+    [[maybe_unused]] long long full_lo = 0, full_hi = 0;  // keys every row may see
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int r = nt * 8 + r8;
+        uint4 raw[HALVES][2];
+        float amax = 0.f;
+#pragma unroll
+        for (int hh = 0; hh < HALVES; ++hh)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                raw[hh][e] = make_uint4(0u, 0u, 0u, 0u);
+                if (r < rows) raw[hh][e] = __ldg(reinterpret_cast<const uint4*>(p.q + row_q(r) + hh * 64 + c4 * 16 + e * 8));
+                const uint32_t w[4] = {raw[hh][e].x, raw[hh][e].y, raw[hh][e].z, raw[hh][e].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
+            }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const int e2 = row_exponent(amax);
+        const float down = pow2f(-e2);
+        const float up = p.scale_log2 * pow2f(e2);
+        cq[nt][0] = __shfl_sync(0xffffffffu, up, 8 * c4);
+        cq[nt][1] = __shfl_sync(0xffffffffu, up, 8 * c4 + 4);
+#pragma unroll
+        for (int hh = 0; hh < HALVES; ++hh)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint4& v = raw[hh][j >> 1];
+                const uint32_t w0 = (j & 1) ? v.z : v.x, w1 = (j & 1) ? v.w : v.y;
+                qf[nt][hh][j][0] = pack_f16x2(__uint_as_float(w0 << 16) * down, __uint_as_float(w0 & 0xFFFF0000u) * down);
+                qf[nt][hh][j][1] = pack_f16x2(__uint_as_float(w1 << 16) * down, __uint_as_float(w1 & 0xFFFF0000u) * down);
+            }
+        if constexpr (kMasked) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int rr = nt * 8 + 2 * c4 + e;
+                long long lo = sp.k_lo, hi = sp.k_lo;  // rows of the padding see nothing
+                if (rr < rows) key_range(p, sq, (row0 + rr) / p.g, &lo, &hi);
+                klo[nt][e] = static_cast<int>(lo - sp.k_lo);
+                khi[nt][e] = static_cast<int>(hi - sp.k_lo);
+            }
+        }
+    }
+    if constexpr (kMasked) {
+        long long lo, hi;
+        key_range(p, sq, (row0 + rows - 1) / p.g, &full_lo, &hi);
+        key_range(p, sq, row0 / p.g, &lo, &full_hi);
+    }
+
+    float my[NT][2], l[NT][2], acc[NT][MT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        my[nt][0] = my[nt][1] = -CUDART_INF_F;
+        l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[nt][i][e] = 0.f;
+    }
+
+#pragma unroll 1
+    for (int i = 0; i < nsteps; ++i) {
+        cp_async_wait<T::STAGES - 2>();
+        __syncwarp();  // the scales were copied by lanes 0 and 1
+        issue(i + T::STAGES - 1);
+        const uint32_t slot = ring + (i % T::STAGES) * T::KV_BYTES;
+        const float2 sc = lds_f2(sring + (i % T::STAGES) * 8);
+        const long long key0 = (sp.first + static_cast<long long>(i) * DP8_WARPS + warp) * DP8_BLOCK;
+
+        // S^T = K Q^T
+        float s[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+#pragma unroll
+        for (int hh = 0; hh < HALVES; ++hh) {
+            const uint4 ka = lds_u4(slot + (hh * 32 + lane) * 16), kb = lds_u4(slot + ((HALVES + hh) * 32 + lane) * 16);
+            const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t a0 = e4m3x2_to_f16x2(wa[j]), a2 = e4m3x2_hi_to_f16x2(wa[j]);
+                const uint32_t a1 = e4m3x2_to_f16x2(wb[j]), a3 = e4m3x2_hi_to_f16x2(wb[j]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt], a0, a1, a2, a3, qf[nt][hh][j][0], qf[nt][hh][j][1]);
+            }
+        }
+
+        // V codes of this lane's rows and columns
+        uint32_t vw[4][T::VB / 4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t a = slot + DP8_BLOCK * D + (e * 32 + lane) * T::VB;
+            if constexpr (D == 128) {
+                const uint4 v = lds_u4(a);
+                vw[e][0] = v.x, vw[e][1] = v.y, vw[e][2] = v.z, vw[e][3] = v.w;
+            } else {
+                const uint2 v = lds_u2(a);
+                vw[e][0] = v.x, vw[e][1] = v.y;
+            }
+        }
+
+        // y = x log2e + log2 vs, with keys a row may not see at -inf
+        const float vs = sc.y < kMinValueScale ? kMinValueScale : sc.y;
+        const float lvs = fast_log2(vs), rvs = __fdividef(1.f, vs);
+        const bool whole = kMasked ? key0 >= full_lo && key0 + DP8_BLOCK <= full_hi : key0 >= sp.k_lo && key0 + DP8_BLOCK <= sp.k_hi;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[nt][e] = fmaf(s[nt][e], cq[nt][e & 1] * sc.x, lvs);
+        if (!whole) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int rel = static_cast<int>(key0 - sp.k_lo) + r8 + 8 * (e >> 1);
+                    if constexpr (kMasked) {
+                        if (rel < klo[nt][e & 1] || rel >= khi[nt][e & 1]) s[nt][e] = -CUDART_INF_F;
+                    } else {
+                        if (rel < 0 || rel >= sp.k_hi - sp.k_lo) s[nt][e] = -CUDART_INF_F;
+                    }
+                }
+        }
+        bool raise = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) raise |= fmaxf(s[nt][e], s[nt][e + 2]) > my[nt][e] + kDp8Slack;
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float m = fmaxf(s[nt][e], s[nt][e + 2]);
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                    m = fmaxf(m, my[nt][e]);
+                    const float alpha = m == my[nt][e] ? 1.f : fast_exp2(my[nt][e] - m);
+                    my[nt][e] = m;
+                    l[nt][e] *= alpha;
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        acc[nt][t][e] *= alpha;
+                        acc[nt][t][e + 2] *= alpha;
+                    }
+                }
+        }
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const float sh0 = kDp8Shift - (my[nt][0] == -CUDART_INF_F ? 0.f : my[nt][0]);
+            const float sh1 = kDp8Shift - (my[nt][1] == -CUDART_INF_F ? 0.f : my[nt][1]);
+            const float p0 = fast_exp2(s[nt][0] + sh0), p1 = fast_exp2(s[nt][1] + sh1);
+            const float p2 = fast_exp2(s[nt][2] + sh0), p3 = fast_exp2(s[nt][3] + sh1);
+            l[nt][0] = fmaf(p0 + p2, rvs, l[nt][0]);
+            l[nt][1] = fmaf(p1 + p3, rvs, l[nt][1]);
+            pf[nt][0] = movmatrix_trans(pack_f16x2(p0, p1));
+            pf[nt][1] = movmatrix_trans(pack_f16x2(p2, p3));
+        }
+
+        if constexpr (kMasked) {
+            // A NaN in a V row that some rows of the tile may not see: take it
+            // out of the product and put it into the rows that see it.
+            if (!whole) {
+                bool bad = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int w = 0; w < T::VB / 4; ++w) bad |= has_nan4(vw[e][w]);
+                if (__any_sync(0xffffffffu, bad)) {
+#pragma unroll
+                    for (int w = 0; w < T::VB / 4; ++w)
+#pragma unroll
+                        for (int byte = 0; byte < 4; ++byte) {
+                            unsigned keys = 0;  // keys of the step whose element w*4 + byte is NaN
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (((vw[e][w] >> (8 * byte)) & 0x7Fu) == 0x7Fu) {
+                                    keys |= 1u << (2 * c4 + (e & 1) + 8 * (e >> 1));
+                                    vw[e][w] &= ~(0xFFu << (8 * byte));
+                                }
+                            keys |= __shfl_xor_sync(0xffffffffu, keys, 1);
+                            keys |= __shfl_xor_sync(0xffffffffu, keys, 2);
+                            // element of this lane: 2t + e of O^T tile t
+                            const int el = w * 4 + byte;
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const int rel = static_cast<int>(key0 - sp.k_lo);
+                                    bool seen = false;
+                                    for (int k = 0; k < DP8_BLOCK; ++k)
+                                        seen |= ((keys >> k) & 1u) && rel + k >= klo[nt][e] && rel + k < khi[nt][e];
+                                    if (seen) acc[nt][el / 2][e + 2 * (el & 1)] = CUDART_NAN_F;
+                                }
+                        }
+                }
+            }
+        }
+
+        // O^T += V^T P^T
+#pragma unroll
+        for (int w = 0; w < T::VB / 4; ++w) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t sel = e == 0 ? 0x5140u : 0x7362u;
+                const uint32_t lo = __byte_perm(vw[0][w], vw[1][w], sel), hi = __byte_perm(vw[2][w], vw[3][w], sel);
+                const uint32_t a0 = e4m3x2_to_f16x2(lo), a1 = e4m3x2_hi_to_f16x2(lo);
+                const uint32_t a2 = e4m3x2_to_f16x2(hi), a3 = e4m3x2_hi_to_f16x2(hi);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma_f16_16816(acc[nt][2 * w + e], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+            }
+        }
+    }
+    cp_async_wait<0>();
+
+    // The warps' states through shared memory (the ring is free now).
+    float* sm_m = reinterpret_cast<float*>(dp8_smem);           // [warp][row]
+    float* sm_l = sm_m + DP8_WARPS * ROWS;                      // [warp][row]
+    float* sm_acc = sm_l + DP8_WARPS * ROWS;                    // [warp][row][D + 4]
+    constexpr int LD = D + 4;
+    static_assert((DP8_WARPS * ROWS * (LD + 2)) * 4 <= T::RING_BYTES, "the warps' states fit the ring");
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float t = l[nt][e];
+            t += __shfl_xor_sync(0xffffffffu, t, 4);
+            t += __shfl_xor_sync(0xffffffffu, t, 8);
+            t += __shfl_xor_sync(0xffffffffu, t, 16);
+            const int r = nt * 8 + 2 * c4 + e;
+            if (r8 == 0) {
+                sm_m[warp * ROWS + r] = my[nt][e];
+                sm_l[warp * ROWS + r] = t;
+            }
+            float* dst = sm_acc + (warp * ROWS + r) * LD + r8 * T::VB;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                dst[2 * i] = acc[nt][i][e];
+                dst[2 * i + 1] = acc[nt][i][e + 2];
+            }
+        }
+    __syncthreads();
+    // Eight elements of a row per thread.
+    for (int w = threadIdx.x; w < rows * (D / 8); w += 32 * DP8_WARPS) {
+        const int r = w / (D / 8), d0 = (w % (D / 8)) * 8;
+        float M = -CUDART_INF_F;
+        bool nan = false;
+#pragma unroll
+        for (int k = 0; k < DP8_WARPS; ++k) M = fmaxf(M, sm_m[k * ROWS + r]);
+        float L = 0.f, f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < DP8_WARPS; ++k) {
+            const float mk = sm_m[k * ROWS + r], lk = sm_l[k * ROWS + r];
+            // a warp whose scores are all NaN has no reference: its l is NaN
+            const float wt = mk == -CUDART_INF_F ? (lk == 0.f ? 0.f : lk) : fast_exp2(mk - M);
+            nan |= wt != wt;
+            L = fmaf(wt, lk, L);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = fmaf(wt, sm_acc[(k * ROWS + r) * LD + d0 + e], f[e]);
+        }
+        const bool empty = M == -CUDART_INF_F && !nan;
+        const float inv = empty ? 0.f : 1.f / L;
+        const float lse2 = empty ? -CUDART_INF_F : M + fast_log2(L) - kDp8Shift;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = empty ? 0.f : f[e] * inv;
+        if (sp.active <= 1) {
+            *reinterpret_cast<uint4*>(p.o + row_q(r) + d0) =
+                make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+            if (d0 == 0 && p.lse != nullptr) p.lse[row_lse(r)] = lse2 * 0.6931471805599453f;
+        } else {
+            const long long at = (row_q(r) / D) * p.S + split;
+            float4* dst = reinterpret_cast<float4*>(p.ws_o + at * D + d0);
+            dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+            dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+            if (d0 == 0) p.ws_lse[at] = lse2;
+        }
+    }
+}
+
+// One row (token, query head) per warp: merge its splits.  grid.x = rows of
+// one sequence and head group in tiles of 4, as the split kernel cut them.
+template <int D>
+__global__ void __launch_bounds__(128) merge_paged_fp8_kernel(const PagedFp8Params p, int tile_rows) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int EPL = D / 32;  // elements per lane
+    const int lane = threadIdx.x & 31;
+    const long long item = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    const int per_seq = p.max_q * p.Hq;
+    const int b = static_cast<int>(item / per_seq), w = static_cast<int>(item % per_seq);
+    if (b >= p.B) return;
+    const SeqSpan sq = seq_span(p, b);
+    const int i = w / p.Hq, hq = w % p.Hq;
+    const int n_tok = sq.n < p.max_q ? sq.n : p.max_q;
+    if (i >= n_tok) return;
+    // the tile of this row, whose union of keys was split
+    const int row = i * p.g + hq % p.g;
+    const int row0 = row / tile_rows * tile_rows;
+    const int rows = n_tok * p.g - row0 < tile_rows ? n_tok * p.g - row0 : tile_rows;
+    const SplitSpan sp = split_span(p, sq, row0 / p.g, (row0 + rows - 1) / p.g, 0);
+    if (sp.active <= 1) return;  // written by the split kernel
+    const long long r = (static_cast<long long>(sq.q0) + i) * p.Hq + hq;
+    const float* ls = p.ws_lse + r * p.S;
+    float M = -CUDART_INF_F;
+    bool nan = false;
+    for (int s = lane; s < sp.active; s += 32) {
+        const float x = ls[s];
+        nan |= x != x;
+        M = fmaxf(M, x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    nan = __any_sync(0xffffffffu, nan);
+    const float safe = M == -CUDART_INF_F ? 0.f : M;
+    float W = 0.f, f[EPL];
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) f[e] = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < sp.active; ++s) {
+        const float wt = fast_exp2(ls[s] - safe);
+        W += wt;
+        const float* src = p.ws_o + (r * p.S + s) * D + lane * EPL;
+        if constexpr (EPL == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(src);
+            f[0] = fmaf(wt, v.x, f[0]), f[1] = fmaf(wt, v.y, f[1]), f[2] = fmaf(wt, v.z, f[2]), f[3] = fmaf(wt, v.w, f[3]);
+        } else {
+            const float2 v = *reinterpret_cast<const float2*>(src);
+            f[0] = fmaf(wt, v.x, f[0]), f[1] = fmaf(wt, v.y, f[1]);
+        }
+    }
+    const bool empty = M == -CUDART_INF_F && !nan;
+    const float inv = empty ? 0.f : 1.f / W;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + r * D + lane * EPL);
+    dst[0] = pack_bf16x2(f[0] * inv, f[1] * inv);
+    if constexpr (EPL == 4) dst[1] = pack_bf16x2(f[2] * inv, f[3] * inv);
+    if (lane == 0 && p.lse != nullptr)
+        p.lse[(static_cast<long long>(sq.q0) + i) * p.lse_tok + static_cast<long long>(hq) * p.lse_head] =
+            empty ? -CUDART_INF_F : (M + fast_log2(W)) * 0.6931471805599453f;
+}
+
+}  // namespace fattn

@@ -17,8 +17,11 @@
 #include "attn_bwd_sm100.cuh"
 #include "attn_fwd_f32.cuh"
 #include "attn_fwd_sm100.cuh"
+#include "decode_paged_fp8.cuh"
 #include "decode_splitkv.cuh"
 #include "fp8_quant.cuh"
+#include "paged_fp8_append.cuh"
+#include "paged_plan.cuh"
 #include "sched.cuh"
 
 namespace {
@@ -126,6 +129,11 @@ int device_ready(DeviceInfo* out) {
             e = e != cudaSuccess ? e : cudaFuncSetAttribute(attn_bwd_sm100_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdTraits<64>::SMEM_BYTES);
             e = e != cudaSuccess ? e : cudaFuncSetAttribute(attn_fwd_f32_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, F32Traits<128>::SMEM_BYTES);
             e = e != cudaSuccess ? e : cudaFuncSetAttribute(attn_fwd_f32_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, F32Traits<64>::SMEM_BYTES);
+            e = e != cudaSuccess ? e : cudaFuncSetAttribute(decode_paged_fp8_kernel<128, 1, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Dp8Traits<128>::SMEM_BYTES);
+            e = e != cudaSuccess ? e : cudaFuncSetAttribute(decode_paged_fp8_kernel<128, 1, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Dp8Traits<128>::SMEM_BYTES);
+            e = e != cudaSuccess ? e : cudaFuncSetAttribute(decode_paged_fp8_kernel<128, 2, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Dp8Traits<128>::SMEM_BYTES);
+            e = e != cudaSuccess ? e : cudaFuncSetAttribute(decode_paged_fp8_kernel<128, 2, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Dp8Traits<128>::SMEM_BYTES);
+            e = e != cudaSuccess ? e : cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * (PLAN_MAX_SEQ + 1) * 4);
             if (e != cudaSuccess) {
                 cudaGetLastError();
                 return FATTN_ERR_CUDA;
@@ -980,3 +988,5 @@ int attn_decode_splitkv_noalloc(const void* q, const void* k_cache, const void* 
 }
 
 }  // extern "C"
+
+#include "paged_api.cuh"

@@ -1,0 +1,296 @@
+// paged_api.cuh -- C ABI of the paged 8-bit cache: plan, append, decode and
+// multi-token attention (declared in include/fattn.h).  Included by
+// fattn_api.cu, whose helpers it uses.
+#pragma once
+
+namespace {
+
+bool pow2_page(int page_size) { return page_size >= 16 && (page_size & (page_size - 1)) == 0; }
+
+int log2_of(int x) {
+    int s = 0;
+    while ((1 << s) < x) ++s;
+    return s;
+}
+
+bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+// Query-row tiles of one sequence and kv head in the split kernel: 8 rows to a
+// CTA while they hold a whole group, else 16.
+int dp8_tile_rows(long long rows) { return rows <= 8 ? 8 : 16; }
+
+int dp8_auto_splits(long long tiles, int Lk) {
+    // CTAs to fill the GPU several times over, so that uneven sequences and
+    // the last wave cost little, with at least 64 keys to a split
+    long long S = (kDp8TargetCtas + tiles - 1) / tiles;
+    const long long most = (static_cast<long long>(Lk) + 63) / 64;
+    S = S > 64 ? 64 : S;
+    S = S > most ? most : S;
+    return static_cast<int>(S < 1 ? 1 : S);
+}
+
+size_t dp8_workspace(long long rows, int S, int d) {
+    return S <= 1 ? 0 : static_cast<size_t>(rows) * S * (static_cast<size_t>(d) + 1) * sizeof(float);
+}
+
+template <int D, int NT, bool kMasked>
+int launch_dp8_kernel(const PagedFp8Params& p, unsigned grid, cudaStream_t s) {
+    decode_paged_fp8_kernel<D, NT, kMasked><<<grid, 32 * DP8_WARPS, Dp8Traits<D>::SMEM_BYTES, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+}
+
+template <int D>
+int launch_dp8_merge(const PagedFp8Params& p, int tile_rows, cudaStream_t s) {
+    cudaLaunchConfig_t cfg{};
+    const long long items = static_cast<long long>(p.B) * p.max_q * p.Hq;
+    cfg.gridDim = dim3(static_cast<unsigned>((items + 3) / 4));
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, merge_paged_fp8_kernel<D>, p, tile_rows) != cudaSuccess) {
+        cudaGetLastError();
+        return FATTN_ERR_CUDA;
+    }
+    return FATTN_OK;
+}
+
+// Checks shared by the two attention entry points (host only).
+int check_paged_fp8(const void* q, const void* k, const void* v, const float* ks, const float* vs, const int* table,
+                    int max_pages, int page_size, int num_pages, const void* o, const float* lse, const int* seqlens_k,
+                    int B, int Hq, int Hkv, int d, float scale) {
+    if (!q || !k || !v || !ks || !vs || !table || !seqlens_k || !o) return FATTN_ERR_INVALID_ARG;
+    if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_pages < 1 || num_pages < 1) return FATTN_ERR_INVALID_ARG;
+    if (!pow2_page(page_size)) return FATTN_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return FATTN_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return FATTN_ERR_UNSUPPORTED;
+    if (B > 65535 || Hq > 65535 || Hq / Hkv > 128) return FATTN_ERR_UNSUPPORTED;
+    if (static_cast<long long>(max_pages) * page_size > 0x7fffff00 ||
+        static_cast<long long>(num_pages) * page_size > (1LL << 40))
+        return FATTN_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return FATTN_ERR_MISALIGNED;
+    if (misaligned4(ks) || misaligned4(vs) || misaligned4(table) || misaligned4(seqlens_k) || (lse && misaligned4(lse)))
+        return FATTN_ERR_MISALIGNED;
+    return FATTN_OK;
+}
+
+// The split kernel over the rows of every sequence, and the merge.
+int launch_dp8(PagedFp8Params p, int d, int num_splits, void* workspace, size_t workspace_bytes, void* stream) {
+    const long long rows = static_cast<long long>(p.max_q) * p.g;
+    const int tile_rows = dp8_tile_rows(rows);
+    const long long row_tiles = (rows + tile_rows - 1) / tile_rows;
+    const long long tiles = static_cast<long long>(p.B) * p.Hkv * row_tiles;
+    const int Lk = p.max_pages << p.page_shift;
+    p.S = num_splits > 0 ? num_splits : dp8_auto_splits(tiles, Lk);
+    if (p.S > Lk) return FATTN_ERR_INVALID_ARG;
+    if (tiles * p.S > 0x7fffffffLL || static_cast<long long>(p.B) * p.max_q * p.Hq > 0x7fffffffLL) return FATTN_ERR_UNSUPPORTED;
+    p.row_tiles = static_cast<int>(row_tiles);
+    const long long all_rows = static_cast<long long>(p.total_q) * p.Hq;
+    const size_t need = dp8_workspace(all_rows, p.S, d);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need) return FATTN_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return FATTN_ERR_MISALIGNED;
+        p.ws_o = static_cast<float*>(workspace);
+        p.ws_lse = p.ws_o + all_rows * p.S * d;
+    }
+    DeviceInfo di;
+    int st = device_ready(&di);
+    if (st != FATTN_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const unsigned grid = static_cast<unsigned>(tiles * p.S);
+    const bool masked = p.max_q > 1;
+    if (d == 128) {
+        if (tile_rows == 8) st = masked ? launch_dp8_kernel<128, 1, true>(p, grid, s) : launch_dp8_kernel<128, 1, false>(p, grid, s);
+        else st = masked ? launch_dp8_kernel<128, 2, true>(p, grid, s) : launch_dp8_kernel<128, 2, false>(p, grid, s);
+    } else {
+        if (tile_rows == 8) st = masked ? launch_dp8_kernel<64, 1, true>(p, grid, s) : launch_dp8_kernel<64, 1, false>(p, grid, s);
+        else st = masked ? launch_dp8_kernel<64, 2, true>(p, grid, s) : launch_dp8_kernel<64, 2, false>(p, grid, s);
+    }
+    if (st != FATTN_OK || p.S == 1) return st;
+    return d == 128 ? launch_dp8_merge<128>(p, tile_rows, s) : launch_dp8_merge<64>(p, tile_rows, s);
+}
+
+template <int D, int W>
+int launch_append(const AppendParams& p, cudaStream_t s) {
+    constexpr int UNITS = W == 1 ? 4 : 1;
+    const long long grid = (p.units + UNITS - 1) / UNITS;
+    if (grid > 0x7fffffffLL) return FATTN_ERR_UNSUPPORTED;
+    append_paged_fp8_kernel<D, W><<<static_cast<unsigned>(grid), W == 1 ? 128 : 32 * W, 0, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_paged_plan(const int* seqlens_k, const int* seqlens_new, int B, const int* free_pages, int num_free,
+                    int* block_table, int max_pages, int page_size, long long* slot_map, int max_tokens,
+                    int* cu_seqlens, int* seqlens_out, int* counts, void* stream) {
+    if (!seqlens_k || !seqlens_new || !block_table || !slot_map || !cu_seqlens || !seqlens_out || !counts)
+        return FATTN_ERR_INVALID_ARG;
+    if (B < 1 || num_free < 0 || (num_free > 0 && !free_pages) || max_pages < 1 || max_tokens < 1) return FATTN_ERR_INVALID_ARG;
+    if (!pow2_page(page_size)) return FATTN_ERR_INVALID_ARG;
+    if (B > PLAN_MAX_SEQ || max_tokens > 0x7fffff00) return FATTN_ERR_UNSUPPORTED;
+    if (misaligned4(seqlens_k) || misaligned4(seqlens_new) || misaligned4(free_pages) || misaligned4(block_table) ||
+        misaligned4(cu_seqlens) || misaligned4(seqlens_out) || misaligned4(counts) ||
+        (reinterpret_cast<uintptr_t>(slot_map) & 7u))
+        return FATTN_ERR_MISALIGNED;
+    // the lengths are read while the outputs are written
+    const size_t nb = static_cast<size_t>(B) * 4;
+    if (overlap(seqlens_out, nb, seqlens_k, nb) || overlap(seqlens_out, nb, seqlens_new, nb) ||
+        overlap(cu_seqlens, nb + 4, seqlens_k, nb) || overlap(cu_seqlens, nb + 4, seqlens_new, nb))
+        return FATTN_ERR_INVALID_ARG;
+    DeviceInfo di;
+    const int st = device_ready(&di);
+    if (st != FATTN_OK) return st;
+    PlanParams p{seqlens_k, seqlens_new, free_pages, block_table, slot_map, cu_seqlens, seqlens_out, counts,
+                 B, max_pages, log2_of(page_size), num_free, max_tokens};
+    const unsigned grid = static_cast<unsigned>((static_cast<long long>(max_tokens) + PLAN_TOKENS - 1) / PLAN_TOKENS);
+    paged_plan_kernel<<<grid, PLAN_THREADS, 2 * (nb + 4), static_cast<cudaStream_t>(stream)>>>(p);
+    return cudaGetLastError() == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+}
+
+int attn_append_paged_fp8(const void* k, const void* v, long long k_stride, long long v_stride, const long long* slot_map,
+                          int num_tokens, void* k_pages, void* v_pages, float* k_scales, float* v_scales, int num_pages,
+                          int page_size, int H, int d, void* stream) {
+    if (!k || !v || !slot_map || !k_pages || !v_pages || !k_scales || !v_scales) return FATTN_ERR_INVALID_ARG;
+    if (num_tokens < 1 || num_pages < 1 || H < 1 || !pow2_page(page_size)) return FATTN_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return FATTN_ERR_UNSUPPORTED;
+    const long long row = static_cast<long long>(H) * d;
+    if (H > 65535 || num_tokens > 0x7fffff00 || static_cast<long long>(num_pages) * page_size > (1LL << 40))
+        return FATTN_ERR_UNSUPPORTED;
+    if (num_tokens > 1 && (k_stride < row || v_stride < row)) return FATTN_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_pages) || !aligned16(v_pages) || k_stride % 8 != 0 || v_stride % 8 != 0 ||
+        misaligned4(k_scales) || misaligned4(v_scales) || (reinterpret_cast<uintptr_t>(slot_map) & 7u))
+        return FATTN_ERR_MISALIGNED;
+    const size_t pool = static_cast<size_t>(num_pages) * page_size * row, sc = static_cast<size_t>(num_pages) * H * 4;
+    if (overlap(k_pages, pool, v_pages, pool) || overlap(k_scales, sc, v_scales, sc)) return FATTN_ERR_INVALID_ARG;
+    DeviceInfo di;
+    const int st = device_ready(&di);
+    if (st != FATTN_OK) return st;
+    AppendParams p{};
+    p.x[0] = static_cast<const __nv_bfloat16*>(k);
+    p.x[1] = static_cast<const __nv_bfloat16*>(v);
+    p.stride[0] = k_stride;
+    p.stride[1] = v_stride;
+    p.pages[0] = static_cast<uint8_t*>(k_pages);
+    p.pages[1] = static_cast<uint8_t*>(v_pages);
+    p.scales[0] = k_scales;
+    p.scales[1] = v_scales;
+    p.slots = slot_map;
+    p.num_slots = static_cast<long long>(num_pages) * page_size;
+    p.T = num_tokens;
+    p.H = H;
+    p.page_shift = log2_of(page_size);
+    // warps to a unit so that a page's rows stay in its registers; tokens to a
+    // unit so that the units are about one wave of 64 warps an SM
+    const int W = page_size <= 16 ? 1 : (page_size <= 64 ? 4 : 8);
+    long long chunk = (2LL * H * num_tokens * W + 64LL * di.num_sms - 1) / (64LL * di.num_sms);
+    p.chunk = static_cast<int>(chunk < 1 ? 1 : (chunk > 16 ? 16 : chunk));
+    p.units = (static_cast<long long>(num_tokens) + p.chunk - 1) / p.chunk * H * 2;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (d == 128) return W == 1 ? launch_append<128, 1>(p, s) : (W == 4 ? launch_append<128, 4>(p, s) : launch_append<128, 8>(p, s));
+    return W == 1 ? launch_append<64, 1>(p, s) : (W == 4 ? launch_append<64, 4>(p, s) : launch_append<64, 8>(p, s));
+}
+
+int attn_decode_paged_fp8_auto_splits(int B, int Hq, int Hkv, int Lk, int d) {
+    if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Lk < 1 || (d != 64 && d != 128)) return FATTN_ERR_INVALID_ARG;
+    const long long g = Hq / Hkv;
+    const int t = dp8_tile_rows(g);
+    return dp8_auto_splits(static_cast<long long>(B) * Hkv * ((g + t - 1) / t), Lk);
+}
+
+int attn_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
+                          const float* v_scales, const int* block_table, int max_pages, int page_size, int num_pages,
+                          void* o, float* lse, const int* seqlens_k, int B, int Hq, int Hkv, int d, float scale,
+                          int window_left, int num_splits, void* workspace, size_t workspace_bytes, void* stream) {
+    const int st = check_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, max_pages, page_size, num_pages, o,
+                                   lse, seqlens_k, B, Hq, Hkv, d, scale);
+    if (st != FATTN_OK) return st;
+    if (num_splits < 0) return FATTN_ERR_INVALID_ARG;
+    PagedFp8Params p{};
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k = static_cast<const uint8_t*>(k_pages);
+    p.v = static_cast<const uint8_t*>(v_pages);
+    p.ks = k_scales;
+    p.vs = v_scales;
+    p.block_table = block_table;
+    p.seqlens_k = seqlens_k;
+    p.o = static_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    p.lse_tok = Hq;
+    p.lse_head = 1;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.g = Hq / Hkv;
+    p.total_q = B;
+    p.max_q = 1;
+    p.max_pages = max_pages;
+    p.page_shift = log2_of(page_size);
+    p.num_pages = num_pages;
+    p.causal = 1;
+    p.window_left = window_left < 0 ? -1 : window_left;
+    p.window_right = -1;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    return launch_dp8(p, d, num_splits, workspace, workspace_bytes, stream);
+}
+
+size_t attn_fwd_paged_fp8_workspace_bytes(int B, int total_q, int max_seqlen_q, int Hq, int Hkv, int Lk, int d) {
+    if (B < 1 || total_q < 1 || max_seqlen_q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Lk < 1 || (d != 64 && d != 128))
+        return 0;
+    const long long rows = static_cast<long long>(max_seqlen_q) * (Hq / Hkv);
+    const int t = dp8_tile_rows(rows);
+    const int S = dp8_auto_splits(static_cast<long long>(B) * Hkv * ((rows + t - 1) / t), Lk);
+    return dp8_workspace(static_cast<long long>(total_q) * Hq, S, d);
+}
+
+int attn_fwd_paged_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
+                       const float* v_scales, const int* block_table, int max_pages, int page_size, int num_pages,
+                       void* o, float* lse, const int* seqlens_k, const int* cu_seqlens_q, int B, int total_q,
+                       int max_seqlen_q, int Hq, int Hkv, int d, float scale, int causal, int window_left,
+                       int window_right, void* workspace, size_t workspace_bytes, void* stream) {
+    const int st = check_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, max_pages, page_size, num_pages, o,
+                                   lse, seqlens_k, B, Hq, Hkv, d, scale);
+    if (st != FATTN_OK) return st;
+    if (!cu_seqlens_q || total_q < 1 || max_seqlen_q < 1) return FATTN_ERR_INVALID_ARG;
+    if (misaligned4(cu_seqlens_q)) return FATTN_ERR_MISALIGNED;
+    if (total_q > 0x7fffff00 || max_seqlen_q > 0x7fffff00) return FATTN_ERR_UNSUPPORTED;
+    PagedFp8Params p{};
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k = static_cast<const uint8_t*>(k_pages);
+    p.v = static_cast<const uint8_t*>(v_pages);
+    p.ks = k_scales;
+    p.vs = v_scales;
+    p.block_table = block_table;
+    p.seqlens_k = seqlens_k;
+    p.cu_q = cu_seqlens_q;
+    p.o = static_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    p.lse_tok = 1;
+    p.lse_head = total_q;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.g = Hq / Hkv;
+    p.total_q = total_q;
+    p.max_q = max_seqlen_q < total_q ? max_seqlen_q : total_q;
+    p.max_pages = max_pages;
+    p.page_shift = log2_of(page_size);
+    p.num_pages = num_pages;
+    p.causal = causal ? 1 : 0;
+    p.window_left = window_left < 0 ? -1 : window_left;
+    p.window_right = window_right < 0 ? -1 : window_right;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    return launch_dp8(p, d, 0, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -20,6 +20,7 @@ if not os.path.exists(_LIB_PATH):
 lib = ctypes.CDLL(_LIB_PATH)
 
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_ll = ctypes.c_longlong
 _llp = ctypes.POINTER(ctypes.c_longlong)
 lib.attn_fwd.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _i, _i, _i, _vp]
 lib.attn_fwd.restype = _i
@@ -42,6 +43,20 @@ lib.attn_decode_splitkv_noalloc.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i
 lib.attn_decode_splitkv_noalloc.restype = _i
 lib.attn_decode_paged.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _i, _i, _i, _f, _i, _vp, _sz, _vp]
 lib.attn_decode_paged.restype = _i
+lib.attn_paged_plan.argtypes = [_vp, _vp, _i, _vp, _i, _vp, _i, _i, _vp, _i, _vp, _vp, _vp, _vp]
+lib.attn_paged_plan.restype = _i
+lib.attn_append_paged_fp8.argtypes = [_vp, _vp, _ll, _ll, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp]
+lib.attn_append_paged_fp8.restype = _i
+lib.attn_decode_paged_fp8.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _i,
+                                      _vp, _sz, _vp]
+lib.attn_decode_paged_fp8.restype = _i
+lib.attn_decode_paged_fp8_auto_splits.argtypes = [_i, _i, _i, _i, _i]
+lib.attn_decode_paged_fp8_auto_splits.restype = _i
+lib.attn_fwd_paged_fp8.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f,
+                                   _i, _i, _i, _vp, _sz, _vp]
+lib.attn_fwd_paged_fp8.restype = _i
+lib.attn_fwd_paged_fp8_workspace_bytes.argtypes = [_i, _i, _i, _i, _i, _i, _i]
+lib.attn_fwd_paged_fp8_workspace_bytes.restype = _sz
 lib.attn_decode_auto_splits.argtypes = [_i, _i, _i, _i]
 lib.attn_decode_auto_splits.restype = _i
 lib.attn_decode_workspace_bytes.argtypes = [_i, _i, _i, _i, _i]
@@ -376,6 +391,173 @@ def attn_decode_paged(q, k_pages, v_pages, block_table, seqlens_k, o=None, lse=N
     _check(lib.attn_decode_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), max_pages, page_size,
                                  num_pages, _ptr(o), _ptr(lse), _ptr(seqlens_k), B, H, d, scale, S, _ptr(workspace),
                                  workspace.numel() * workspace.element_size(), _stream()), "attn_decode_paged")
+    return o, lse
+
+
+def _want_current(dev):
+    """The library works on the current device: tensors of another one are refused."""
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def attn_paged_plan(seqlens_k, seqlens_new, free_pages, block_table, page_size, max_tokens, slot_map=None,
+                    cu_seqlens=None, seqlens_out=None, counts=None):
+    """Where the new tokens of a batch go in a paged cache.  seqlens_k,
+    seqlens_new: int32 [B], tokens held and tokens arriving; free_pages: int32
+    [num_free] physical pages not in use; block_table: int32 [B, max_pages],
+    updated in place with the pages taken -> (slot_map int64 [max_tokens],
+    cu_seqlens int32 [B + 1], seqlens_out int32 [B], counts int32 [2]: tokens,
+    pages needed).  Tokens without a page and places behind the last token have
+    slot -1."""
+    _want(seqlens_k, torch.int32, 1, "seqlens_k")
+    dev = seqlens_k.device
+    _want_current(dev)
+    B = seqlens_k.shape[0]
+    _want(seqlens_new, torch.int32, 1, "seqlens_new", shape=(B,), device=dev)
+    _want(free_pages, torch.int32, 1, "free_pages", device=dev)
+    _want(block_table, torch.int32, 2, "block_table", device=dev)
+    max_pages = block_table.shape[1]
+    _want(block_table, torch.int32, 2, "block_table", shape=(B, max_pages))
+    if slot_map is None:
+        slot_map = torch.empty(max_tokens, dtype=torch.int64, device=dev)
+    _want(slot_map, torch.int64, 1, "slot_map", shape=(max_tokens,), device=dev)
+    if cu_seqlens is None:
+        cu_seqlens = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    _want(cu_seqlens, torch.int32, 1, "cu_seqlens", shape=(B + 1,), device=dev)
+    if seqlens_out is None:
+        seqlens_out = torch.empty(B, dtype=torch.int32, device=dev)
+    _want(seqlens_out, torch.int32, 1, "seqlens_out", shape=(B,), device=dev)
+    if counts is None:
+        counts = torch.empty(2, dtype=torch.int32, device=dev)
+    _want(counts, torch.int32, 1, "counts", shape=(2,), device=dev)
+    _check(lib.attn_paged_plan(_ptr(seqlens_k), _ptr(seqlens_new), B, _ptr(free_pages), free_pages.shape[0],
+                               _ptr(block_table), max_pages, page_size, _ptr(slot_map), max_tokens, _ptr(cu_seqlens),
+                               _ptr(seqlens_out), _ptr(counts), _stream()), "attn_paged_plan")
+    return slot_map, cu_seqlens, seqlens_out, counts
+
+
+def _want_cache(k_pages, v_pages, k_scales, v_scales, dev):
+    """The four tensors of a paged 8-bit cache -> (num_pages, page_size, Hkv, d)."""
+    _want(k_pages, torch.uint8, 4, "k_pages", device=dev)
+    shape = k_pages.shape
+    _want(v_pages, torch.uint8, 4, "v_pages", shape=shape, device=dev)
+    _want(k_scales, torch.float32, 2, "k_scales", shape=(shape[0], shape[2]), device=dev)
+    _want(v_scales, torch.float32, 2, "v_scales", shape=(shape[0], shape[2]), device=dev)
+    return shape
+
+
+def _want_rows(t, name, shape, dev):
+    """bf16 rows [tokens, H, d] whose tokens may be apart (a view of a fused
+    projection); the heads of a token are contiguous -> the token stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16 or t.device != dev or tuple(t.shape) != tuple(shape) or t.stride(2) != 1 \
+            or (shape[1] > 1 and t.stride(1) != shape[2]) or (shape[0] > 1 and t.stride(0) < shape[1] * shape[2]):
+        raise ValueError(f"{name}: expected bf16 rows {tuple(shape)} on {dev} with contiguous heads, got "
+                         f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
+    return t.stride(0) if shape[0] > 1 else shape[1] * shape[2]
+
+
+def attn_append_paged_fp8(k, v, slot_map, k_pages, v_pages, k_scales, v_scales):
+    """Quantize new rows into a paged 8-bit cache, in place.  k, v: bf16
+    [tokens, Hkv, d] (token stride free); slot_map: int64 [tokens] (the first
+    tokens of a longer map are taken as a slice); k_pages, v_pages: uint8 e4m3
+    codes [num_pages, page_size, Hkv, d]; k_scales, v_scales: fp32
+    [num_pages, Hkv]."""
+    _want(slot_map, torch.int64, 1, "slot_map")
+    dev = slot_map.device
+    _want_current(dev)
+    num_pages, page_size, H, d = _want_cache(k_pages, v_pages, k_scales, v_scales, dev)
+    tokens = slot_map.shape[0]
+    ks, vs = _want_rows(k, "k", (tokens, H, d), dev), _want_rows(v, "v", (tokens, H, d), dev)
+    _check(lib.attn_append_paged_fp8(_ptr(k), _ptr(v), ks, vs, _ptr(slot_map), tokens, _ptr(k_pages), _ptr(v_pages),
+                                     _ptr(k_scales), _ptr(v_scales), num_pages, page_size, H, d, _stream()),
+           "attn_append_paged_fp8")
+
+
+def attn_decode_paged_fp8_auto_splits(B, Hq, Hkv, Lk, d) -> int:
+    return lib.attn_decode_paged_fp8_auto_splits(B, Hq, Hkv, Lk, d)
+
+
+def attn_decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, o=None, lse=None, scale=None,
+                          window_left=-1, num_splits=0, workspace=None):
+    """Split-KV decode over a paged 8-bit cache.  q: bf16 [B,Hq,1,d]; cache as
+    attn_append_paged_fp8; block_table: int32 [B, max_pages]; seqlens_k: int32
+    [B], the new token included -> (o [B,Hq,1,d], lse [B,Hq])."""
+    _want(q, torch.bfloat16, 4, "q")
+    B, Hq, Lq, d = q.shape
+    dev = q.device
+    _want_current(dev)
+    if Lq != 1:
+        raise ValueError(f"q: decode takes one query per head, got Lq={Lq}")
+    num_pages, page_size, Hkv, dk = _want_cache(k_pages, v_pages, k_scales, v_scales, dev)
+    if dk != d or Hkv == 0 or Hq % Hkv:
+        raise ValueError(f"k_pages: heads of {dk} elements, {Hkv} of them, do not serve {Hq} query heads of {d}")
+    _want(block_table, torch.int32, 2, "block_table", device=dev)
+    max_pages = block_table.shape[1]
+    _want(block_table, torch.int32, 2, "block_table", shape=(B, max_pages))
+    _want(seqlens_k, torch.int32, 1, "seqlens_k", shape=(B,), device=dev)
+    if o is None:
+        o = torch.empty_like(q)
+    _want(o, torch.bfloat16, 4, "o", shape=(B, Hq, 1, d), device=dev)
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+    _want(lse, torch.float32, 2, "lse", shape=(B, Hq), device=dev)
+    Lk = max_pages * page_size
+    S = num_splits if num_splits != 0 else attn_decode_paged_fp8_auto_splits(B, Hq, Hkv, Lk, d)
+    if workspace is None and S > 1:
+        workspace = torch.empty(attn_decode_workspace_bytes(B, Hq, Lk, d, S), dtype=torch.uint8, device=dev)
+    _want_workspace(workspace, dev)
+    scale = (1.0 / d ** 0.5) if scale is None else scale
+    _check(lib.attn_decode_paged_fp8(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales),
+                                     _ptr(block_table), max_pages, page_size, num_pages, _ptr(o), _ptr(lse),
+                                     _ptr(seqlens_k), B, Hq, Hkv, d, scale, int(window_left), S, _ptr(workspace),
+                                     0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                     _stream()), "attn_decode_paged_fp8")
+    return o, lse
+
+
+def attn_fwd_paged_fp8_workspace_bytes(B, total_q, max_seqlen_q, Hq, Hkv, Lk, d) -> int:
+    return lib.attn_fwd_paged_fp8_workspace_bytes(B, total_q, max_seqlen_q, Hq, Hkv, Lk, d)
+
+
+def attn_fwd_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, cu_seqlens_q, max_seqlen_q,
+                       o=None, lse=None, scale=None, causal=False, window_left=-1, window_right=-1, workspace=None):
+    """Packed prefill over a paged 8-bit cache.  q: bf16 [total_q, Hq, d], the
+    new tokens of all sequences; cu_seqlens_q: int32 [B + 1]; seqlens_k: int32
+    [B], the new tokens included; cache and block_table as
+    attn_decode_paged_fp8 -> (o [total_q, Hq, d], lse [Hq, total_q])."""
+    _want(q, torch.bfloat16, 3, "q")
+    total_q, Hq, d = q.shape
+    dev = q.device
+    _want_current(dev)
+    num_pages, page_size, Hkv, dk = _want_cache(k_pages, v_pages, k_scales, v_scales, dev)
+    if dk != d or Hkv == 0 or Hq % Hkv:
+        raise ValueError(f"k_pages: heads of {dk} elements, {Hkv} of them, do not serve {Hq} query heads of {d}")
+    _want(seqlens_k, torch.int32, 1, "seqlens_k", device=dev)
+    B = seqlens_k.shape[0]
+    _want(block_table, torch.int32, 2, "block_table", device=dev)
+    max_pages = block_table.shape[1]
+    _want(block_table, torch.int32, 2, "block_table", shape=(B, max_pages))
+    _want(cu_seqlens_q, torch.int32, 1, "cu_seqlens_q", shape=(B + 1,), device=dev)
+    if o is None:
+        o = torch.empty_like(q)
+    _want(o, torch.bfloat16, 3, "o", shape=(total_q, Hq, d), device=dev)
+    if lse is None:
+        lse = torch.empty((Hq, total_q), dtype=torch.float32, device=dev)
+    _want(lse, torch.float32, 2, "lse", shape=(Hq, total_q), device=dev)
+    if workspace is None:
+        need = attn_fwd_paged_fp8_workspace_bytes(B, total_q, max_seqlen_q, Hq, Hkv, max_pages * page_size, d)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _want_workspace(workspace, dev)
+    scale = (1.0 / d ** 0.5) if scale is None else scale
+    _check(lib.attn_fwd_paged_fp8(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales),
+                                  _ptr(block_table), max_pages, page_size, num_pages, _ptr(o), _ptr(lse),
+                                  _ptr(seqlens_k), _ptr(cu_seqlens_q), B, total_q, int(max_seqlen_q), Hq, Hkv, d, scale,
+                                  int(bool(causal)), int(window_left), int(window_right), _ptr(workspace),
+                                  0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                  _stream()), "attn_fwd_paged_fp8")
     return o, lse
 
 

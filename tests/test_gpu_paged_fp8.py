@@ -1,0 +1,563 @@
+"""The paged 8-bit KV cache on the GPU (plan, append, decode, multi-token
+attention) against the plain 64-bit implementations of tests/_paged_ref.py."""
+import math
+
+import pytest
+import torch
+
+from tests import _paged_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fl():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from io_aware_exact_34_b200 import build
+    build.build()
+    from io_aware_exact_34_b200 import fattn
+    return fattn
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _table(lens, page, width, pages, g):
+    """Distinct random pages for every sequence's length; -1 elsewhere."""
+    order = torch.randperm(pages, generator=g).tolist()
+    out = []
+    for n in lens:
+        k = -(-n // page)
+        out.append([order.pop() for _ in range(k)] + [-1] * (width - k))
+    return out
+
+
+def _cache(pages, page, hkv, d, g, spread=2):
+    """Random codes (no NaN) and power-of-two scales 2^-7 * 2^[-spread, spread]."""
+    def codes():
+        c = torch.randint(0, 256, (pages, page, hkv, d), generator=g, dtype=torch.int32)
+        x = torch.randn(c.shape, generator=g) * 90.0  # the values a quantizer leaves
+        return x.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    def scales():
+        return torch.exp2(torch.randint(-7 - spread, -7 + spread + 1, (pages, hkv), generator=g).float())
+    return codes(), codes(), scales(), scales()
+
+
+# ---------------------------------------------------------------- plan
+PLAN_CASES = {
+    "one": ([0], [1], 16, 2, 4, 1),
+    "decode": ([31, 32, 33, 0, 15], [1] * 5, 16, 4, 8, 5),
+    "prompts": ([0, 100, 64, 7], [300, 0, 129, 1000], 64, 17, 40, 1500),
+    "short capacity": ([5, 9], [40, 40], 16, 8, 9, 50),
+    "short free list": ([5, 9, 0], [40, 40, 40], 16, 8, 4, 130),
+    "no free list": ([5, 16], [3, 3], 16, 8, 0, 8),
+    "short table": ([5, 9], [100, 3], 32, 2, 9, 110),
+    "negative": ([-3, 20], [4, -5], 16, 4, 3, 9),
+    "nothing": ([3, 4], [0, 0], 16, 4, 3, 2),
+}
+
+
+@pytest.mark.parametrize("name", PLAN_CASES)
+def test_plan_matches_reference(fl, name):
+    lens, new, page, width, nfree, room = PLAN_CASES[name]
+    g = torch.Generator().manual_seed(len(name))
+    table = _table([max(0, min(x, width * page)) for x in lens], page, width, 64, g)
+    free = [100 + int(i) for i in torch.randperm(nfree, generator=g)]
+    dev = _i32(table)
+    slots, cu, out, counts = fl.attn_paged_plan(_i32(lens), _i32(new), _i32(free), dev, page, room)
+    e_slots, e_cu, e_out, e_counts, e_table = ref.plan(lens, new, free, table, page, room)
+    assert slots.tolist() == e_slots and cu.tolist() == e_cu and out.tolist() == e_out
+    assert counts.tolist() == e_counts and dev.tolist() == e_table
+
+
+@pytest.mark.parametrize("B,longest,new,page", [(1, 1, 20000, 16), (257, 500, 90, 32), (4096, 64, 1, 16), (16384, 300, 3, 128)])
+def test_plan_sizes(fl, B, longest, new, page):
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, longest + 1, (B,), generator=g).tolist()
+    adds = torch.randint(0, new + 1, (B,), generator=g).tolist()
+    adds[-1] = new
+    width = -(-(longest + new) // page)
+    held = sum(-(-x // page) for x in lens)
+    table = _table(lens, page, width, held, g)
+    need = sum(-(-(x + a) // page) - -(-x // page) for x, a in zip(lens, adds))
+    free = (held + torch.randperm(need, generator=g)).tolist()
+    room = sum(adds) + 3
+    dev = _i32(table)
+    slots, cu, out, counts = fl.attn_paged_plan(_i32(lens), _i32(adds), _i32(free), dev, page, room)
+    e = ref.plan(lens, adds, free, table, page, room)
+    for x, y in zip((slots, cu, out, counts, dev), e):
+        assert x.tolist() == y
+
+
+def test_plan_saturates(fl):
+    """Sums beyond 31 bits are written as 2^31 - 1 and reach no memory."""
+    lens, new = [2 ** 31 - 5, 2 ** 31 - 1, 3], [2 ** 31 - 1, 7, 2]
+    table = _i32([[0, 1]] * 3)
+    slots, cu, out, counts = fl.attn_paged_plan(_i32(lens), _i32(new), _i32([5, 6]), table, 16, 64)
+    assert slots.tolist() == [-1] * 64 and cu.tolist() == [0] + [2 ** 31 - 1] * 3
+    assert out.tolist() == [2 ** 31 - 1, 2 ** 31 - 1, 5] and counts[0] == 2 ** 31 - 1
+    assert table.tolist() == [[0, 1]] * 3
+
+
+# ---------------------------------------------------------------- append
+def _append_and_check(fl, x, slots, cache, page):
+    """x: bf16 (k, v) on the GPU, any token stride; cache: CPU codes and scales."""
+    kc, vc, ks, vs = [t.cuda() for t in cache]
+    fl.attn_append_paged_fp8(x[0], x[1], torch.tensor(slots, dtype=torch.int64, device="cuda"), kc, vc, ks, vs)
+    for t, c, s, c0, s0 in ((x[0], kc, ks, cache[0], cache[2]), (x[1], vc, vs, cache[1], cache[3])):
+        values, scales = ref.value(c0), s0.double()
+        ref.append(t.double().cpu(), slots, values, scales)
+        assert torch.equal(s.double().cpu(), scales)
+        assert torch.equal(ref.value(c.cpu()).nan_to_num(1e9), values.nan_to_num(1e9))
+    return kc, vc, ks, vs
+
+
+@pytest.mark.parametrize("lens,new,page,hkv,d", [
+    ([0], [1], 16, 1, 128), ([15, 16, 17, 0, 3], [1] * 5, 16, 8, 128), ([3, 0, 40], [50, 16, 9], 16, 2, 64),
+    ([0, 100, 31, 64], [200, 1, 90, 64], 64, 3, 128), ([250, 0], [300, 513], 256, 2, 128), ([1, 0, 129], [700, 256, 1], 256, 1, 64),
+    ([7, 8], [33, 1], 32, 5, 64), ([100], [1000], 128, 4, 128), ([0], [1500], 1024, 1, 128),
+])
+def test_append_matches_reference(fl, lens, new, page, hkv, d):
+    g = torch.Generator().manual_seed(sum(lens) + page)
+    full = [a + b for a, b in zip(lens, new)]
+    width, pages = max(-(-x // page) for x in full), sum(-(-x // page) for x in full) + 2
+    table = _table(full, page, width, pages, g)
+    slots = [table[b][p // page] * page + p % page for b in range(len(lens)) for p in range(lens[b], full[b])]
+    cache = _cache(pages, page, hkv, d, g)
+    x = torch.randn(len(slots), 2, hkv, d, generator=g) * torch.exp(2 * torch.randn(len(slots), 1, 1, 1, generator=g))
+    x = x.to(torch.bfloat16).cuda()  # K and V interleaved: token stride 2 * hkv * d
+    _append_and_check(fl, (x[:, 0], x[:, 1]), slots, cache, page)
+    _append_and_check(fl, (x[:, 0].contiguous(), x[:, 1].contiguous()), slots, cache, page)
+
+
+def test_append_skips_and_duplicates(fl):
+    """Slots outside the pool are skipped; one named again in a stretch keeps the later token."""
+    g = torch.Generator().manual_seed(1)
+    cache = _cache(6, 16, 2, 128, g)
+    slots = [-1, 5 * 16 + 3, 5 * 16 + 4, 96, -7, 16, 17, 17, 17, 18, 10 ** 12, 3 * 16 + 15, 40, 40]
+    x = torch.randn(len(slots), 2, 2, 128, generator=g).to(torch.bfloat16).cuda()
+    _append_and_check(fl, (x[:, 0], x[:, 1]), slots, cache, 16)
+    slots = [20] * 70  # longer than a page, one row
+    x = torch.randn(len(slots), 2, 2, 128, generator=g).to(torch.bfloat16).cuda()
+    _append_and_check(fl, (x[:, 0], x[:, 1]), slots, cache, 16)
+
+
+def test_append_extremes(fl):
+    """Zeros, subnormals, the largest bf16, exact scale borders, infinities and NaN."""
+    g = torch.Generator().manual_seed(2)
+    H, d = 2, 64
+    rows = [torch.zeros(H, d), torch.full((H, d), 1e-39), torch.full((H, d), 3.3895e38), torch.full((H, d), 448.0 * 2.0 ** -9),
+            torch.full((H, d), 450.0 * 2.0 ** -9), torch.full((H, d), -1.75), torch.randn(H, d, generator=g) * 1e-30]
+    bad = torch.randn(H, d, generator=g)
+    bad[0, 3], bad[0, 5], bad[1, 7] = math.inf, -math.inf, math.nan
+    rows += [bad, torch.full((H, d), math.nan)]
+    for i, r in enumerate(rows):
+        cache = _cache(3, 16, H, d, g)
+        x = r[None].to(torch.bfloat16).cuda()
+        for slot in (16, 16 + 5):  # a fresh page, and one with rows before
+            _append_and_check(fl, (x, x), [slot], cache, 16)
+    # all of them one after the other into one page: the scale grows over the whole range
+    cache = _cache(3, 16, H, d, g)
+    for i, r in enumerate(rows):
+        x = r[None].to(torch.bfloat16).cuda()
+        kc, vc, ks, vs = _append_and_check(fl, (x, x), [32 + i], cache, 16)
+        cache = (kc.cpu(), vc.cpu(), ks.cpu(), vs.cpu())
+
+
+def test_append_leaves_the_rest(fl):
+    """Other pages, other heads' scales and rows behind the new ones keep their bytes."""
+    g = torch.Generator().manual_seed(4)
+    cache = _cache(5, 32, 3, 128, g)
+    kc, vc, ks, vs = [t.cuda() for t in cache]
+    x = (torch.randn(4, 3, 128, generator=g) * 100).to(torch.bfloat16).cuda()
+    fl.attn_append_paged_fp8(x, x, torch.arange(2 * 32 + 8, 2 * 32 + 12, device="cuda"), kc, vc, ks, vs)
+    for new, old in ((kc, cache[0]), (vc, cache[1])):
+        new = new.cpu()
+        assert torch.equal(new[[0, 1, 3, 4]], old[[0, 1, 3, 4]]) and torch.equal(new[2, 12:], old[2, 12:])
+        assert not torch.equal(new[2, 8:12], old[2, 8:12])
+    for new, old in ((ks, cache[2]), (vs, cache[3])):
+        assert torch.equal(new.cpu()[[0, 1, 3, 4]], old[[0, 1, 3, 4]])
+
+
+def test_append_rejects(fl):
+    g = torch.Generator().manual_seed(5)
+    kc, vc, ks, vs = [t.cuda() for t in _cache(3, 16, 2, 64, g)]
+    x = torch.zeros(2, 2, 64, dtype=torch.bfloat16, device="cuda")
+    slots = torch.zeros(2, dtype=torch.int64, device="cuda")
+    for bad in ((x[:1], x), (x.transpose(1, 2).contiguous().transpose(1, 2), x), (x.half(), x), (x.cpu(), x)):
+        with pytest.raises((ValueError, TypeError), match="k:"):
+            fl.attn_append_paged_fp8(*bad, slots, kc, vc, ks, vs)
+    with pytest.raises(ValueError, match="v_scales:"):
+        fl.attn_append_paged_fp8(x, x, slots, kc, vc, ks, vs[:2])
+    with pytest.raises(ValueError, match="v_pages:"):
+        fl.attn_append_paged_fp8(x, x, slots, kc, vc[:, :8], ks, vs)
+    with pytest.raises(ValueError, match="slot_map:"):
+        fl.attn_append_paged_fp8(x, x, slots.int(), kc, vc, ks, vs)
+    with pytest.raises(fl.FattnError):
+        fl.attn_append_paged_fp8(x, x, slots, kc, kc, ks, vs)
+    odd = torch.zeros(2, 2 * 64 + 4, dtype=torch.bfloat16, device="cuda")[:, :128].view(2, 2, 64)
+    with pytest.raises(fl.FattnError):
+        fl.attn_append_paged_fp8(odd, x, slots, kc, vc, ks, vs)
+
+
+# ---------------------------------------------------------------- attention
+def _check_rows(o, lse, exp, d, length, label=""):
+    """o [n, Hq, d], lse [n, Hq] of the GPU against ref.attention's answer."""
+    eo, el, w, dots = exp
+    o, lse = o.double().cpu(), lse.double().cpu()
+    empty = el == -math.inf
+    assert torch.equal(lse == -math.inf, empty), label
+    assert bool((o[empty] == 0).all()), label
+    bad = eo.isnan()
+    assert torch.equal(o.isnan(), bad), label
+    to, tl = ref.tolerances(eo, w, dots, d, max(1, length))
+    far = torch.where(bad, 0.0, (o - eo).abs() - to)
+    assert float(far.max()) <= 0.0, f"{label}: O off by {float(far.max()):.3e} more than its bound"
+    fine = ~empty & ~el.isnan()
+    if fine.any():
+        far = ((lse - el).abs() - tl)[fine]
+        assert float(far.max()) <= 0.0, f"{label}: LSE off by {float(far.max()):.3e} more than its bound"
+
+
+def _decode_case(fl, lens, page, hq, hkv, d, seed, left=-1, splits=0, spread=2, spoil=True, q_gain=1.0):
+    g = torch.Generator().manual_seed(seed)
+    width = max(1, max(-(-x // page) for x in lens)) + 1
+    pages = sum(-(-x // page) for x in lens) + 2
+    table = _table(lens, page, width, pages, g)
+    kc, vc, ks, vs = _cache(pages, page, hkv, d, g, spread)
+    q = (torch.randn(len(lens), hq, 1, d, generator=g) * q_gain).to(torch.bfloat16)
+    if spoil:
+        # rows behind the lengths and pages no table names: NaN codes and NaN scales
+        named = torch.zeros(pages, dtype=torch.bool)
+        for b, n in enumerate(lens):
+            for p in range(-(-n // page)):
+                named[table[b][p]] = True
+                kc[table[b][p], max(0, n - p * page):] = 0x7F
+                vc[table[b][p], max(0, n - p * page):] = 0xFF
+        for t in (ks, vs):
+            t[~named] = math.nan
+        for t in (kc, vc):
+            t[~named] = 0x7F
+    o, lse = fl.attn_decode_paged_fp8(q.cuda(), kc.cuda(), vc.cuda(), ks.cuda(), vs.cuda(), _i32(table), _i32(lens),
+                                      window_left=left, num_splits=splits)
+    kv, vv = ref.value(kc), ref.value(vc)
+    for b, n in enumerate(lens):
+        exp = ref.attention(q[b, :, 0].double()[None], ref.gather(kv, ks.double(), table[b], n), ref.gather(vv, vs.double(), table[b], n),
+                            float(torch.tensor(d ** -0.5, dtype=torch.float32)), left=left)
+        _check_rows(o[b, :, 0][None], lse[b][None], exp, d, n, f"sequence {b} of {n} keys")
+
+
+@pytest.mark.parametrize("lens,page,hq,hkv,d,left,splits", [
+    ([1], 16, 1, 1, 128, -1, 0), ([0, 1, 15, 16, 17, 63, 64, 65], 16, 4, 1, 128, -1, 0), ([0, 0], 16, 2, 2, 64, -1, 0),
+    ([300, 5, 1000], 16, 8, 8, 128, -1, 1), ([300, 5, 1000], 16, 8, 8, 64, -1, 3), ([4097, 2], 64, 32, 8, 128, -1, 0),
+    ([777, 1555], 256, 16, 2, 128, -1, 7), ([777, 1555], 32, 16, 1, 64, -1, 0), ([130, 1029], 128, 12, 4, 128, -1, 0),
+    ([500], 16, 10, 2, 64, -1, 2), ([999, 48], 16, 32, 1, 128, -1, 0), ([333], 16, 71, 1, 64, -1, 0), ([40, 200], 16, 128, 1, 128, -1, 0),
+    ([1000, 3, 129, 0], 16, 8, 2, 128, 100, 0), ([1000, 128], 64, 8, 8, 64, 0, 0), ([2000, 77], 32, 16, 16, 128, 1023, 4),
+    ([1 << 14], 16, 8, 2, 128, -1, 64),
+])
+def test_decode_matches_reference(fl, lens, page, hq, hkv, d, left, splits):
+    _decode_case(fl, lens, page, hq, hkv, d, seed=sum(lens) + hq, left=left, splits=splits)
+
+
+@pytest.mark.parametrize("spread,q_gain", [(20, 1.0), (5, 30.0), (0, 1e-20), (2, 0.0)])
+def test_decode_ranges(fl, spread, q_gain):
+    """Page scales far apart, sharp and flat softmax rows."""
+    _decode_case(fl, [700, 65, 2100], 16, 8, 2, 128, seed=9, spread=spread, q_gain=q_gain)
+    _decode_case(fl, [700, 65, 2100], 32, 16, 1, 64, seed=9, spread=spread, q_gain=q_gain)
+
+
+def test_decode_not_power_of_two_scales(fl):
+    g = torch.Generator().manual_seed(11)
+    lens, page = [100, 515], 16
+    pages = sum(-(-x // page) for x in lens)
+    table = _table(lens, page, 33, pages, g)
+    kc, vc, _, _ = _cache(pages, page, 2, 128, g)
+    ks, vs = [torch.rand(pages, 2, generator=g) * 0.02 + 1e-4 for _ in range(2)]
+    q = torch.randn(2, 8, 1, 128, generator=g).to(torch.bfloat16)
+    o, lse = fl.attn_decode_paged_fp8(q.cuda(), kc.cuda(), vc.cuda(), ks.cuda(), vs.cuda(), _i32(table), _i32(lens), scale=0.25)
+    for b, n in enumerate(lens):
+        exp = ref.attention(q[b, :, 0].double()[None], ref.gather(ref.value(kc), ks.double(), table[b], n),
+                            ref.gather(ref.value(vc), vs.double(), table[b], n), 0.25)
+        _check_rows(o[b, :, 0][None], lse[b][None], exp, 128, n)
+
+
+def test_decode_visible_nan(fl):
+    """A NaN in a visible K row spoils its head's rows; one in V only its column; a NaN query only itself."""
+    g = torch.Generator().manual_seed(12)
+    lens, page = [100, 200], 16
+    pages = sum(-(-x // page) for x in lens)
+    table = _table(lens, page, 14, pages, g)
+    kc, vc, ks, vs = _cache(pages, page, 2, 128, g)
+    kc[table[0][2], 3, 1, 9] = 0x7F
+    vc[table[1][4], 7, 0, 77] = 0xFF
+    q = torch.randn(2, 8, 1, 128, generator=g).to(torch.bfloat16)
+    q[1, 6, 0, 5] = math.nan
+    for splits in (0, 1, 2):
+        o, lse = fl.attn_decode_paged_fp8(q.cuda(), kc.cuda(), vc.cuda(), ks.cuda(), vs.cuda(), _i32(table), _i32(lens), num_splits=splits)
+        want = torch.zeros(2, 8, 1, 128, dtype=torch.bool)
+        want[0, 4:] = True
+        want[1, :4, 0, 77] = True
+        want[1, 6] = True
+        assert torch.equal(o.isnan().cpu(), want)
+        assert torch.equal(lse.isnan().cpu(), want.all(-1)[..., 0])
+
+
+def test_decode_bad_tables_and_lengths(fl):
+    """Table entries outside the pool are clamped, lengths beyond the table too: same as with the clamped ones."""
+    g = torch.Generator().manual_seed(13)
+    kc, vc, ks, vs = [t.cuda() for t in _cache(6, 16, 2, 64, g)]
+    q = torch.randn(2, 4, 1, 64, generator=g).to(torch.bfloat16).cuda()
+    a = fl.attn_decode_paged_fp8(q, kc, vc, ks, vs, _i32([[-5, 2, 99], [3, 1 << 30, 0]]), _i32([1000, -4]))
+    b = fl.attn_decode_paged_fp8(q, kc, vc, ks, vs, _i32([[0, 2, 5], [3, 5, 0]]), _i32([48, 0]))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert bool((a[0][1] == 0).all()) and bool((a[1][1] == -math.inf).all())
+
+
+def test_decode_far_offsets(fl):
+    """Pages whose byte offsets pass 32 bits."""
+    hkv, d, page = 8, 128, 256
+    pages = (5 << 30) // (page * hkv * d)
+    kc = torch.empty(pages, page, hkv, d, dtype=torch.uint8, device="cuda")
+    vc = torch.empty_like(kc)
+    ks, vs = torch.empty(pages, hkv, device="cuda"), torch.empty(pages, hkv, device="cuda")
+    g = torch.Generator().manual_seed(14)
+    small = _cache(3, page, hkv, d, g)
+    at = torch.tensor([pages - 1, 3, pages - 2], device="cuda")
+    for big, t in zip((kc, vc, ks, vs), small):
+        big[at] = t.cuda()
+    q = torch.randn(1, 32, 1, d, generator=g).to(torch.bfloat16).cuda()
+    a = fl.attn_decode_paged_fp8(q, kc, vc, ks, vs, at.int()[None], _i32([700]))
+    b = fl.attn_decode_paged_fp8(q, *[t.cuda() for t in small], _i32([[0, 1, 2]]), _i32([700]))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    x = torch.randn(2, hkv, d, generator=g).to(torch.bfloat16).cuda()
+    fl.attn_append_paged_fp8(x, x, torch.tensor([pages * page - 2, pages * page - 1], device="cuda"), kc, vc, ks, vs)
+    want = [t.cuda() for t in small]
+    fl.attn_append_paged_fp8(x, x, torch.tensor([254, 255], device="cuda"), *want)
+    assert torch.equal(kc[-1], want[0][0]) and torch.equal(vs[-1], want[3][0])
+
+
+def test_decode_rejects(fl):
+    g = torch.Generator().manual_seed(15)
+    kc, vc, ks, vs = [t.cuda() for t in _cache(3, 16, 2, 64, g)]
+    q = torch.zeros(2, 4, 1, 64, dtype=torch.bfloat16, device="cuda")
+    bt, lens = _i32([[0, 1], [2, 0]]), _i32([20, 3])
+    call = lambda **kw: fl.attn_decode_paged_fp8(**{**dict(q=q, k_pages=kc, v_pages=vc, k_scales=ks, v_scales=vs, block_table=bt, seqlens_k=lens), **kw})  # noqa: E731
+    call()
+    for bad, match in ((dict(q=q[:, :3].contiguous()), "k_pages:"), (dict(q=q.repeat(1, 1, 2, 1)), "one query"), (dict(q=q[..., :32].contiguous()), "k_pages:"),
+                       (dict(block_table=bt[:1]), "block_table:"), (dict(seqlens_k=lens[:1]), "seqlens_k:"), (dict(k_scales=ks[:, :1].contiguous()), "k_scales:"),
+                       (dict(v_pages=vc.float()), "v_pages:"), (dict(o=q[:1]), "o:"), (dict(lse=torch.zeros(2, 3, device="cuda")), "lse:"),
+                       (dict(workspace=torch.zeros(8)), "workspace:")):
+        with pytest.raises(ValueError, match=match):
+            call(**bad)
+    for bad in (dict(num_splits=-1), dict(num_splits=33), dict(scale=-1.0), dict(num_splits=2, workspace=torch.zeros(16, device="cuda"))):
+        with pytest.raises(fl.FattnError):
+            call(**bad)
+
+
+# ---------------------------------------------------------------- several tokens
+def _fwd_case(fl, lens, new, page, hq, hkv, d, seed, causal=True, left=-1, right=-1, behind=0, most=None, spread=2, nan_v=None):
+    g = torch.Generator().manual_seed(seed)
+    width = max(1, max(-(-x // page) for x in lens)) + 1
+    pages = sum(-(-x // page) for x in lens) + 1
+    table = _table(lens, page, width, pages, g)
+    kc, vc, ks, vs = _cache(pages, page, hkv, d, g, spread)
+    for b, n in enumerate(lens):
+        if n % page:
+            kc[table[b][n // page], n % page:] = 0x7F
+            vc[table[b][n // page], n % page:] = 0x7F
+    for b, pos, h, e in nan_v or []:
+        vc[table[b][pos // page], pos % page, h, e] = 0x7F
+    total = sum(new) + behind
+    q = torch.randn(total, hq, d, generator=g).to(torch.bfloat16)
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    o = torch.full((total, hq, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((hq, total), 7.0, device="cuda")
+    most = max(1, max(new)) if most is None else most
+    fl.attn_fwd_paged_fp8(q.cuda(), kc.cuda(), vc.cuda(), ks.cuda(), vs.cuda(), _i32(table), _i32(lens), _i32(cu), most, o=o, lse=lse,
+                          causal=causal, window_left=left, window_right=right)
+    kv, vv = ref.value(kc), ref.value(vc)
+    for b, n in enumerate(new):
+        if n == 0:
+            continue
+        exp = ref.attention(q[cu[b]:cu[b + 1]].double(), ref.gather(kv, ks.double(), table[b], lens[b]),
+                            ref.gather(vv, vs.double(), table[b], lens[b]), float(torch.tensor(d ** -0.5, dtype=torch.float32)),
+                            causal=causal, left=left, right=right)
+        m = min(n, most)
+        _check_rows(o[cu[b]:cu[b] + m], lse[:, cu[b]:cu[b] + m].T, [t[:m] for t in exp], d, lens[b], f"sequence {b}: {n} of {lens[b]}")
+        assert bool((o[cu[b] + m:cu[b + 1]] == 7).all()) and bool((lse[:, cu[b] + m:cu[b + 1]] == 7).all())
+    assert bool((o[sum(new):] == 7).all()) and bool((lse[:, sum(new):] == 7).all())
+
+
+FWD_CASES = [
+    # lens, new, page, hq, hkv, d, mask
+    ([1], [1], 16, 1, 1, 128, {}), ([40, 5, 0, 17], [3, 5, 0, 1], 16, 4, 2, 128, {}), ([300, 129], [2, 129], 16, 8, 8, 64, {}),
+    ([1000, 33, 512], [5, 5, 4], 16, 32, 8, 128, {}), ([700, 64], [300, 64], 64, 8, 1, 128, {}), ([257, 1111], [257, 140], 32, 6, 2, 64, {}),
+    ([500], [260], 256, 5, 1, 128, {}), ([300], [37], 16, 71, 1, 64, {}), ([140], [9], 16, 128, 1, 128, {}),
+    ([900, 100], [400, 100], 16, 4, 4, 128, dict(left=64)), ([900, 100], [130, 1], 64, 8, 2, 64, dict(left=0)),
+    ([300, 50], [200, 50], 16, 4, 2, 128, dict(causal=False)), ([300, 50], [200, 50], 16, 4, 2, 64, dict(causal=False, left=30, right=20)),
+    ([20, 0, 3], [50, 7, 3], 16, 4, 2, 128, {}), ([20, 5], [50, 9], 16, 2, 1, 64, dict(left=3)), ([5], [300], 16, 4, 1, 128, dict(causal=False, right=2)),
+    ([600, 80], [256, 80], 128, 16, 4, 128, dict(behind=5)), ([600, 80], [256, 20], 16, 4, 2, 128, dict(most=33)),
+    ([900], [300], 16, 4, 2, 128, dict(spread=20)),
+]
+
+
+@pytest.mark.parametrize("lens,new,page,hq,hkv,d,kw", FWD_CASES)
+def test_fwd_matches_reference(fl, lens, new, page, hq, hkv, d, kw):
+    _fwd_case(fl, lens, new, page, hq, hkv, d, seed=sum(lens) + hq, **kw)
+
+
+@pytest.mark.parametrize("hq,hkv,d,new", [(4, 2, 128, 5), (4, 1, 64, 3), (4, 2, 128, 200), (8, 2, 64, 150)])
+def test_fwd_nan_values_spare_rows_that_do_not_see_them(fl, hq, hkv, d, new):
+    """A NaN in V reaches its column in the rows that see its key, and no other row."""
+    _fwd_case(fl, [300, 220], [new, 1], 16, hq, hkv, d, seed=3, nan_v=[(0, 298, hkv - 1, 5), (0, 300 - new, 0, 0), (1, 219, 0, d - 1)])
+    _fwd_case(fl, [300], [new], 16, hq, hkv, d, seed=4, left=40, nan_v=[(0, 290, 0, 1), (0, 300 - new - 20, hkv - 1, 2)])
+
+
+def test_fwd_one_token_is_decode(fl):
+    """One new token per sequence: the rows of attn_decode_paged_fp8, bit for bit when both choose the same splits."""
+    g = torch.Generator().manual_seed(21)
+    lens, page, hq, hkv, d = [900, 31, 16, 2048], 16, 8, 2, 128
+    pages = sum(-(-x // page) for x in lens)
+    table = _i32(_table(lens, page, 128, pages, g))
+    cache = [t.cuda() for t in _cache(pages, page, hkv, d, g)]
+    q = torch.randn(4, hq, 1, d, generator=g).to(torch.bfloat16).cuda()
+    o, lse = fl.attn_decode_paged_fp8(q, *cache, table, _i32(lens))
+    o2, lse2 = fl.attn_fwd_paged_fp8(q[:, :, 0].contiguous(), *cache, table, _i32(lens), _i32([0, 1, 2, 3, 4]), 1, causal=True)
+    assert torch.equal(o[:, :, 0], o2) and torch.equal(lse, lse2.T)
+
+
+def test_fwd_rejects(fl):
+    g = torch.Generator().manual_seed(22)
+    kc, vc, ks, vs = [t.cuda() for t in _cache(3, 16, 2, 64, g)]
+    q = torch.zeros(6, 4, 64, dtype=torch.bfloat16, device="cuda")
+    bt, lens, cu = _i32([[0, 1], [2, 0]]), _i32([20, 3]), _i32([0, 4, 6])
+    call = lambda **kw: fl.attn_fwd_paged_fp8(**{**dict(q=q, k_pages=kc, v_pages=vc, k_scales=ks, v_scales=vs, block_table=bt, seqlens_k=lens, cu_seqlens_q=cu, max_seqlen_q=4, causal=True), **kw})  # noqa: E731
+    call()
+    for bad, match in ((dict(q=q[:, :3].contiguous()), "k_pages:"), (dict(cu_seqlens_q=cu[:2]), "cu_seqlens_q:"), (dict(block_table=bt[:1]), "block_table:"),
+                       (dict(o=q[:5]), "o:"), (dict(lse=torch.zeros(6, 4, device="cuda")), "lse:"), (dict(v_scales=ks[:2]), "v_scales:")):
+        with pytest.raises(ValueError, match=match):
+            call(**bad)
+    for bad in (dict(max_seqlen_q=0), dict(scale=0.0)):
+        with pytest.raises(fl.FattnError):
+            call(**bad)
+
+
+# ---------------------------------------------------------------- as they are used
+def _serve(fl, steps, page, hq, hkv, d, seed):
+    """A prompt batch, then decode steps, then drafted tokens: every step plans, appends and attends."""
+    g = torch.Generator().manual_seed(seed)
+    B, width, pages = 3, 24, 60
+    table = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    free = torch.randperm(pages, generator=g).int().cuda()
+    cache = [torch.full((pages, page, hkv, d), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    cache += [torch.full((pages, hkv), math.nan, device="cuda") for _ in range(2)]
+    values = [torch.zeros(pages, page, hkv, d, dtype=torch.float64) for _ in range(2)]
+    scales = [torch.zeros(pages, hkv, dtype=torch.float64) for _ in range(2)]
+    host_lens, host_table, host_free = [0] * B, [[-1] * width for _ in range(B)], free.tolist()
+    for new in steps:
+        T = sum(new)
+        slots, cu, out, counts = fl.attn_paged_plan(lens, _i32(new), free, table, page, T + 2)
+        e = ref.plan(host_lens, new, host_free, host_table, page, T + 2)
+        assert slots.tolist() == e[0] and table.tolist() == e[4] and counts.tolist() == e[3]
+        kv = (torch.randn(T + 2, 2, hkv, d, generator=g) * torch.exp(torch.randn(T + 2, 1, 1, 1, generator=g))).to(torch.bfloat16)
+        dkv = kv.cuda()
+        fl.attn_append_paged_fp8(dkv[:, 0], dkv[:, 1], slots, *cache)
+        for i in range(2):
+            ref.append(kv[:, i].double(), e[0], values[i], scales[i])
+        q = torch.randn(T, hq, d, generator=g).to(torch.bfloat16)
+        if all(n == 1 for n in new):
+            o, lse = fl.attn_decode_paged_fp8(q[:, :, None].cuda(), *cache, table, out)
+            o = o[:, :, 0]
+        else:
+            o, lse = fl.attn_fwd_paged_fp8(q.cuda(), *cache, table, out, cu, max(new), causal=True)
+            lse = lse.T
+        lens, free = out, free[counts.tolist()[1]:].contiguous()
+        host_lens, host_table, host_free = e[2], e[4], host_free[e[3][1]:]
+        for b, n in enumerate(new):
+            if n == 0:
+                continue
+            exp = ref.attention(q[e[1][b]:e[1][b + 1]].double(), ref.gather(values[0], scales[0], host_table[b], host_lens[b]),
+                                ref.gather(values[1], scales[1], host_table[b], host_lens[b]), float(torch.tensor(d ** -0.5, dtype=torch.float32)))
+            _check_rows(o[e[1][b]:e[1][b + 1]], lse[e[1][b]:e[1][b + 1]], exp, d, host_lens[b], f"step {new}, sequence {b}")
+
+
+def test_serving_run(fl):
+    _serve(fl, [[37, 5, 150], [1, 1, 1], [1, 1, 1], [4, 2, 3], [1, 1, 1], [60, 0, 17], [1, 1, 1]], 16, 8, 2, 128, seed=31)
+    _serve(fl, [[200, 1, 90], [1, 1, 1], [130, 3, 0]], 64, 4, 4, 64, seed=32)
+
+
+def test_captured_step(fl):
+    """Plan, append and decode in one CUDA graph: replays take the lengths and rows that the buffers hold then."""
+    g = torch.Generator().manual_seed(41)
+    B, page, hq, hkv, d, width, pages = 2, 16, 8, 2, 128, 8, 20
+    table = _i32([[0, 1] + [-1] * 6, [2] + [-1] * 7])
+    lens, new, free = _i32([31, 16]), _i32([1, 1]), _i32(list(range(3, 20)))
+    cache = [t.cuda() for t in _cache(pages, page, hkv, d, g)]
+    kv = torch.randn(B, 2, hkv, d, generator=g).to(torch.bfloat16).cuda()
+    q = torch.randn(B, hq, 1, d, generator=g).to(torch.bfloat16).cuda()
+    step = lambda: fl.attn_paged_plan(lens, new, free, table, page, B)  # noqa: E731
+
+    def run():
+        slots, cu, out, counts = step()
+        fl.attn_append_paged_fp8(kv[:, 0], kv[:, 1], slots, *cache)
+        return fl.attn_decode_paged_fp8(q, *cache, table, out) + (out, counts)
+
+    start = [t.clone() for t in [table, lens, free, *cache]]
+
+    def reset():
+        for t, s in zip([table, lens, free, *cache], start):
+            t.copy_(s)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    reset()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run()
+    inputs = [(torch.randn_like(kv), torch.randn_like(q)) for _ in range(3)]
+    seen = []
+    for x, y in inputs:
+        kv.copy_(x), q.copy_(y)
+        graph.replay()
+        seen.append([t.clone() for t in held])
+        lens.copy_(held[2])
+        n = int(held[3][1])
+        free[:free.numel() - n] = free[n:].clone()
+    reset()
+    for (x, y), got in zip(inputs, seen):
+        kv.copy_(x), q.copy_(y)
+        want = run()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        lens.copy_(want[2])
+        n = int(want[3][1])
+        free[:free.numel() - n] = free[n:].clone()
+
+
+def test_other_stream(fl):
+    """Calls on a side stream, two at once with workspaces of their own."""
+    g = torch.Generator().manual_seed(42)
+    lens, page = [3000, 2500], 16
+    pages = sum(-(-x // page) for x in lens)
+    table = _i32(_table(lens, page, 190, pages, g))
+    cache = [t.cuda() for t in _cache(pages, page, 2, 128, g)]
+    qs = [torch.randn(2, 8, 1, 128, generator=g).to(torch.bfloat16).cuda() for _ in range(2)]
+    want = [fl.attn_decode_paged_fp8(q, *cache, table, _i32(lens)) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    for _ in range(5):
+        got = []
+        for s, q in zip(streams, qs):
+            with torch.cuda.stream(s):
+                got.append(fl.attn_decode_paged_fp8(q, *cache, table, _i32(lens)))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
