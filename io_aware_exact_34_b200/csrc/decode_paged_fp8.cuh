@@ -21,17 +21,22 @@
 // largest element); P is rounded to f16 (relative 2^-11).  The key rows are the
 // M operand and 8 query rows the N operand: S^T = K Q^T and O^T = V^T P^T waste
 // nothing at 8 rows a group, where Q as the M operand would pay for 16.
-// A decode step reads 2*d bytes per key and kv head and is bound by that;
-// tcgen05 would add nothing here but the round trip through tensor memory.
+// (mma.sync on e4m3 operands, with Q as two e4m3 terms, was measured: it is
+// expanded to conversions and f16 products, 9 % more instructions.)  A decode
+// step reads 2*d bytes per key and kv head and is bound by that and by the
+// conversions; tcgen05 would add nothing here but the round trip through
+// tensor memory.
 //
 // Loads: a warp takes 16 keys a step (16 divides every page, so one page and
-// one pair of scales per step) through a ring of cp.async stages in shared
-// memory.  Every lane copies exactly the bytes it reads back itself, so the
-// ring needs no barrier between lanes (only the two scales are shared by the
-// warp), and the fragments need no transposition:
-//   K: lane (r = lane/4, c = lane%4) holds 16 bytes of rows r and r + 8 per
+// one pair of scales per step) through its own ring of cp.async stages in
+// shared memory.  Each copy instruction covers whole rows (128 bytes to eight
+// lanes): on B200 that streams 6.9 TB/s, while copies laid out like the
+// fragments, half a row or a column of rows at a time, stop at 5.3 TB/s.  The
+// 16-byte chunks are swizzled so that the fragment reads are free of bank
+// conflicts, and the fragments need no transposition:
+//   K: lane (r = lane/4, c = lane%4) reads 16 bytes of rows r and r + 8 per
 //      64-byte half; the product's k index runs over d in that order, for Q too;
-//   V: the lane holds D/8 bytes of rows 2c, 2c+1, 2c+8, 2c+9; PRMT pairs the
+//   V: the lane reads D/8 bytes of rows 2c, 2c+1, 2c+8, 2c+9; PRMT pairs the
 //      bytes of two rows, and a pair converts to one A register of V^T;
 //   P: S^T's accumulator transposes to the B operand of O^T by movmatrix.
 // Rows outside the keys that some row of the tile may see are filled with
@@ -53,8 +58,9 @@ namespace fattn {
 
 constexpr int DP8_WARPS = 4;
 constexpr int DP8_BLOCK = 16;       // keys per warp step
-constexpr int DP8_MIN_BLOCKS = 4;   // key blocks of the smallest split: one per warp
-constexpr int kDp8TargetCtas = 4096;  // CTAs the automatic split aims at
+constexpr int DP8_MIN_BLOCKS = 16;  // key blocks of the smallest split: 256 keys
+// CTAs the automatic split aims at: 2.9 waves of 3 CTAs on 148 SMs.
+constexpr int kDp8TargetCtas = 1280;
 constexpr float kDp8Shift = 7.f;    // p' = 2^(y - my + 7)
 constexpr float kDp8Slack = 8.f;
 constexpr float kMinValueScale = 7.888609052210118e-31f;  // 2^-100: smaller V scales count as this
@@ -145,14 +151,26 @@ struct Dp8Traits {
     static constexpr int RING_BYTES = DP8_WARPS * WARP_BYTES;
     static constexpr int SCALE_BYTES = DP8_WARPS * STAGES * 8;
     static constexpr int SMEM_BYTES = RING_BYTES + SCALE_BYTES;
+    static constexpr int CPR = D / 16;   // 16-byte chunks per row
+    static constexpr int RPC = 32 / CPR; // rows per copy instruction
+    // Place of a 16-byte chunk in a stage: rows back to back, chunks exchanged
+    // inside each 128-byte line so that the eight lanes of a read phase (K: two
+    // rows of four chunks; V: rows 0, 2, 4, 6 of two chunks) hit all banks.
+    __device__ static __forceinline__ uint32_t k_at(int row, int chunk) {
+        return D == 128 ? row * 128 + ((chunk ^ ((row & 1) << 2)) << 4) : row * 64 + (chunk << 4);
+    }
+    __device__ static __forceinline__ uint32_t v_at(int row, int chunk) {
+        const int line = D == 128 ? row : row >> 1, pos = D == 128 ? chunk : (row & 1) * 4 + chunk;
+        return DP8_BLOCK * D + line * 128 + ((pos ^ (((row >> 1) & 3) << 1)) << 4);
+    }
 };
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
@@ -212,14 +230,13 @@ __device__ __forceinline__ float fast_log2(float x) {
 // True if one of the four bytes is e4m3's NaN (0x7F with either sign).
 __device__ __forceinline__ bool has_nan4(uint32_t w) { return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0; }
 
-// The power of two 2^-e and e for a row's largest magnitude, so that the row
-// times 2^-e has its largest element in [1, 2).
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// The exponent of a row's largest magnitude: the row times 2^-e has it in [1, 2).
 __device__ __forceinline__ int row_exponent(float amax) {
-    int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+    const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
     return e < -100 ? -100 : (e > 126 ? 126 : e);
 }
-
-__device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
 // NT tiles of 8 query rows per CTA.  kMasked: rows of the tile may see
 // different keys (more than one token per sequence).
@@ -267,40 +284,53 @@ __global__ void __launch_bounds__(32 * DP8_WARPS) decode_paged_fp8_kernel(const 
     const long long head_row = static_cast<long long>(p.Hkv) * D;  // bytes between a head's rows
     const int* table = p.block_table + static_cast<long long>(b) * p.max_pages;
 
+    // keys of a step relative to the union's first; the union holds k_len keys
+    const int k_len = static_cast<int>(sp.k_hi - sp.k_lo);
+    const int rel_first = static_cast<int>((sp.first + warp) * DP8_BLOCK - sp.k_lo);
+    auto rel_of = [&](int i) { return rel_first + i * (DP8_WARPS * DP8_BLOCK); };
+    const int page_mask = (1 << shift) - 1;
+    const int key_first = static_cast<int>((sp.first + warp) * DP8_BLOCK);  // absolute: tables hold at most 2^31 keys
+    const int cr = lane / T::CPR, cc = lane % T::CPR;  // row and chunk of this lane in a copy
+    const long long lane_off = static_cast<long long>(h) * D + cr * head_row + cc * 16;
+    const uint8_t *k_lane = p.k + lane_off, *v_lane = p.v + lane_off;
+    const long long copy_step = T::RPC * head_row;
     int table_lane = 0;  // lane i: the page of step 32*(issued/32) + i
     auto issue = [&](int i) {
         if ((i & 31) == 0) {
-            const long long blk = sp.first + static_cast<long long>(i + lane) * DP8_WARPS + warp;
-            if (blk < sp.last) {
-                const int pg = __ldg(table + ((blk * DP8_BLOCK) >> shift));
+            const int mine = i + lane;
+            if (mine < nsteps) {
+                const int pg = __ldg(table + ((key_first + mine * (DP8_WARPS * DP8_BLOCK)) >> shift));
                 table_lane = pg < 0 ? 0 : (pg >= p.num_pages ? p.num_pages - 1 : pg);
             }
         }
         if (i < nsteps) {
-            const long long key0 = (sp.first + static_cast<long long>(i) * DP8_WARPS + warp) * DP8_BLOCK;
-            const long long page = __shfl_sync(0xffffffffu, table_lane, i & 31);
-            const long long row = (page << shift) + (key0 & ((1LL << shift) - 1));
-            const long long at = (row * p.Hkv + h) * D;
+            const int page = __shfl_sync(0xffffffffu, table_lane, i & 31);
+            const int off = (key_first + i * (DP8_WARPS * DP8_BLOCK)) & page_mask;
+            const long long at = ((static_cast<long long>(page) << shift) + off) * head_row;
+            const uint8_t *kp = k_lane + at, *vp = v_lane + at;
             const uint32_t slot = ring + (i % T::STAGES) * T::KV_BYTES;
-            auto there = [&](int r) { return key0 + r >= sp.k_lo && key0 + r < sp.k_hi; };
+            const int rel = rel_of(i);
+            if (rel >= 0 && rel + DP8_BLOCK <= k_len) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = r8 + 8 * e;
-                const uint8_t* src = p.k + at + r * head_row + c4 * 16;
+                for (int e = 0; e < DP8_BLOCK / T::RPC; ++e) {
+                    cp_async16(slot + T::k_at(e * T::RPC + cr, cc), kp);
+                    cp_async16(slot + T::v_at(e * T::RPC + cr, cc), vp);
+                    kp += copy_step;
+                    vp += copy_step;
+                }
+            } else {
 #pragma unroll
-                for (int hh = 0; hh < HALVES; ++hh)
-                    cp_async16(slot + ((e * HALVES + hh) * 32 + lane) * 16, src + hh * 64, there(r) ? 16 : 0);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = 2 * c4 + (e & 1) + 8 * (e >> 1);
-                const uint8_t* src = p.v + at + r * head_row + r8 * T::VB;
-                const uint32_t dst = slot + DP8_BLOCK * D + (e * 32 + lane) * T::VB;
-                if constexpr (D == 128) cp_async16(dst, src, there(r) ? 16 : 0);
-                else cp_async8(dst, src, there(r) ? 8 : 0);
+                for (int e = 0; e < DP8_BLOCK / T::RPC; ++e) {
+                    const int r = rel + e * T::RPC + cr;
+                    const int bytes = r >= 0 && r < k_len ? 16 : 0;
+                    cp_async16(slot + T::k_at(e * T::RPC + cr, cc), kp, bytes);
+                    cp_async16(slot + T::v_at(e * T::RPC + cr, cc), vp, bytes);
+                    kp += copy_step;
+                    vp += copy_step;
+                }
             }
             const uint32_t sslot = sring + (i % T::STAGES) * 8;
-            if (lane < 2) cp_async4(sslot + 4 * lane, (lane == 0 ? p.ks : p.vs) + page * p.Hkv + h);
+            if (lane < 2) cp_async4(sslot + 4 * lane, (lane == 0 ? p.ks : p.vs) + static_cast<long long>(page) * p.Hkv + h);
         }
         cp_async_commit();
     };
@@ -311,7 +341,7 @@ __global__ void __launch_bounds__(32 * DP8_WARPS) decode_paged_fp8_kernel(const 
     uint32_t qf[NT][HALVES][4][2];
     float cq[NT][2];  // scale * log2e * 2^e of the rows 2*c4, 2*c4 + 1
     [[maybe_unused]] int klo[NT][2], khi[NT][2];  // keys of those rows, relative to the union's first key
-    [[maybe_unused]] long long full_lo = 0, full_hi = 0;  // keys every row may see
+    [[maybe_unused]] int full_lo = 0, full_hi = 0;  // keys every row may see, relative too
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int r = nt * 8 + r8;
@@ -356,9 +386,11 @@ __global__ void __launch_bounds__(32 * DP8_WARPS) decode_paged_fp8_kernel(const 
         }
     }
     if constexpr (kMasked) {
-        long long lo, hi;
-        key_range(p, sq, (row0 + rows - 1) / p.g, &full_lo, &hi);
-        key_range(p, sq, row0 / p.g, &lo, &full_hi);
+        long long lo0, hi0, lo1, hi1;
+        key_range(p, sq, row0 / p.g, &lo0, &hi0);
+        key_range(p, sq, (row0 + rows - 1) / p.g, &lo1, &hi1);
+        full_lo = static_cast<int>(lo1 - sp.k_lo);
+        full_hi = static_cast<int>(hi0 - sp.k_lo);
     }
 
     float my[NT][2], l[NT][2], acc[NT][MT][4];
@@ -375,28 +407,28 @@ __global__ void __launch_bounds__(32 * DP8_WARPS) decode_paged_fp8_kernel(const 
 #pragma unroll 1
     for (int i = 0; i < nsteps; ++i) {
         cp_async_wait<T::STAGES - 2>();
-        __syncwarp();  // the scales were copied by lanes 0 and 1
+        __syncwarp();  // a lane reads what others copied
         issue(i + T::STAGES - 1);
         const uint32_t slot = ring + (i % T::STAGES) * T::KV_BYTES;
         const float2 sc = lds_f2(sring + (i % T::STAGES) * 8);
-        const long long key0 = (sp.first + static_cast<long long>(i) * DP8_WARPS + warp) * DP8_BLOCK;
+        const int rel = rel_of(i);
 
         // S^T = K Q^T
-        float s[NT][4];
+        float s[NT][2][4];  // two chains of products, summed below
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+            for (int e = 0; e < 4; ++e) s[nt][0][e] = s[nt][1][e] = 0.f;
 #pragma unroll
         for (int hh = 0; hh < HALVES; ++hh) {
-            const uint4 ka = lds_u4(slot + (hh * 32 + lane) * 16), kb = lds_u4(slot + ((HALVES + hh) * 32 + lane) * 16);
+            const uint4 ka = lds_u4(slot + T::k_at(r8, hh * 4 + c4)), kb = lds_u4(slot + T::k_at(r8 + 8, hh * 4 + c4));
             const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const uint32_t a0 = e4m3x2_to_f16x2(wa[j]), a2 = e4m3x2_hi_to_f16x2(wa[j]);
                 const uint32_t a1 = e4m3x2_to_f16x2(wb[j]), a3 = e4m3x2_hi_to_f16x2(wb[j]);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt], a0, a1, a2, a3, qf[nt][hh][j][0], qf[nt][hh][j][1]);
+                for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt][j & 1], a0, a1, a2, a3, qf[nt][hh][j][0], qf[nt][hh][j][1]);
             }
         }
 
@@ -404,34 +436,35 @@ __global__ void __launch_bounds__(32 * DP8_WARPS) decode_paged_fp8_kernel(const 
         uint32_t vw[4][T::VB / 4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const uint32_t a = slot + DP8_BLOCK * D + (e * 32 + lane) * T::VB;
+            const int r = 2 * c4 + (e & 1) + 8 * (e >> 1);
             if constexpr (D == 128) {
-                const uint4 v = lds_u4(a);
+                const uint4 v = lds_u4(slot + T::v_at(r, r8));
                 vw[e][0] = v.x, vw[e][1] = v.y, vw[e][2] = v.z, vw[e][3] = v.w;
             } else {
-                const uint2 v = lds_u2(a);
+                const uint2 v = lds_u2(slot + T::v_at(r, r8 >> 1) + (r8 & 1) * 8);
                 vw[e][0] = v.x, vw[e][1] = v.y;
             }
         }
 
         // y = x log2e + log2 vs, with keys a row may not see at -inf
+        float y[NT][4];
         const float vs = sc.y < kMinValueScale ? kMinValueScale : sc.y;
         const float lvs = fast_log2(vs), rvs = __fdividef(1.f, vs);
-        const bool whole = kMasked ? key0 >= full_lo && key0 + DP8_BLOCK <= full_hi : key0 >= sp.k_lo && key0 + DP8_BLOCK <= sp.k_hi;
+        const bool whole = kMasked ? rel >= full_lo && rel + DP8_BLOCK <= full_hi : rel >= 0 && rel + DP8_BLOCK <= k_len;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[nt][e] = fmaf(s[nt][e], cq[nt][e & 1] * sc.x, lvs);
+            for (int e = 0; e < 4; ++e) y[nt][e] = fmaf(s[nt][0][e] + s[nt][1][e], cq[nt][e & 1] * sc.x, lvs);
         if (!whole) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int rel = static_cast<int>(key0 - sp.k_lo) + r8 + 8 * (e >> 1);
+                    const int k = rel + r8 + 8 * (e >> 1);
                     if constexpr (kMasked) {
-                        if (rel < klo[nt][e & 1] || rel >= khi[nt][e & 1]) s[nt][e] = -CUDART_INF_F;
+                        if (k < klo[nt][e & 1] || k >= khi[nt][e & 1]) y[nt][e] = -CUDART_INF_F;
                     } else {
-                        if (rel < 0 || rel >= sp.k_hi - sp.k_lo) s[nt][e] = -CUDART_INF_F;
+                        if (k < 0 || k >= k_len) y[nt][e] = -CUDART_INF_F;
                     }
                 }
         }
@@ -439,13 +472,13 @@ __global__ void __launch_bounds__(32 * DP8_WARPS) decode_paged_fp8_kernel(const 
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) raise |= fmaxf(s[nt][e], s[nt][e + 2]) > my[nt][e] + kDp8Slack;
+            for (int e = 0; e < 2; ++e) raise |= fmaxf(y[nt][e], y[nt][e + 2]) > my[nt][e] + kDp8Slack;
         if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float m = fmaxf(s[nt][e], s[nt][e + 2]);
+                    float m = fmaxf(y[nt][e], y[nt][e + 2]);
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
@@ -465,8 +498,8 @@ __global__ void __launch_bounds__(32 * DP8_WARPS) decode_paged_fp8_kernel(const 
         for (int nt = 0; nt < NT; ++nt) {
             const float sh0 = kDp8Shift - (my[nt][0] == -CUDART_INF_F ? 0.f : my[nt][0]);
             const float sh1 = kDp8Shift - (my[nt][1] == -CUDART_INF_F ? 0.f : my[nt][1]);
-            const float p0 = fast_exp2(s[nt][0] + sh0), p1 = fast_exp2(s[nt][1] + sh1);
-            const float p2 = fast_exp2(s[nt][2] + sh0), p3 = fast_exp2(s[nt][3] + sh1);
+            const float p0 = fast_exp2(y[nt][0] + sh0), p1 = fast_exp2(y[nt][1] + sh1);
+            const float p2 = fast_exp2(y[nt][2] + sh0), p3 = fast_exp2(y[nt][3] + sh1);
             l[nt][0] = fmaf(p0 + p2, rvs, l[nt][0]);
             l[nt][1] = fmaf(p1 + p3, rvs, l[nt][1]);
             pf[nt][0] = movmatrix_trans(pack_f16x2(p0, p1));
@@ -502,7 +535,6 @@ __global__ void __launch_bounds__(32 * DP8_WARPS) decode_paged_fp8_kernel(const 
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                                 for (int e = 0; e < 2; ++e) {
-                                    const int rel = static_cast<int>(key0 - sp.k_lo);
                                     bool seen = false;
                                     for (int k = 0; k < DP8_BLOCK; ++k)
                                         seen |= ((keys >> k) & 1u) && rel + k >= klo[nt][e] && rel + k < khi[nt][e];

@@ -25,10 +25,15 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 int dp8_tile_rows(long long rows) { return rows <= 8 ? 8 : 16; }
 
 int dp8_auto_splits(long long tiles, int Lk) {
-    // CTAs to fill the GPU several times over, so that uneven sequences and
-    // the last wave cost little, with at least 64 keys to a split
-    long long S = (kDp8TargetCtas + tiles - 1) / tiles;
-    const long long most = (static_cast<long long>(Lk) + 63) / 64;
+    // About kDp8TargetCtas CTAs: several waves, so that uneven sequences even
+    // out, without many short splits; a split holds at least 256 keys (the
+    // kernel keeps to that by each sequence's own length).  Measured at 3 to
+    // 16 splits of 256 tiles: 32 x 32768 keys 344-355 us at 5-16 splits, 361-370
+    // at 3-4, 369-379 at 24-32; 32 sequences of 1-8192 keys 62-63 us at 4-6
+    // splits, 66 at 3, 70-107 at 12-32; one sequence of 4097 keys (8 tiles):
+    // 10.2 us at 16 splits, 11.7 at 8 and at 32.
+    long long S = (kDp8TargetCtas + tiles / 2) / tiles;
+    const long long most = (static_cast<long long>(Lk) + DP8_MIN_BLOCKS * DP8_BLOCK - 1) / (DP8_MIN_BLOCKS * DP8_BLOCK);
     S = S > 64 ? 64 : S;
     S = S > most ? most : S;
     return static_cast<int>(S < 1 ? 1 : S);

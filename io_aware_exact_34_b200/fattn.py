@@ -394,10 +394,30 @@ def attn_decode_paged(q, k_pages, v_pages, block_table, seqlens_k, o=None, lse=N
     return o, lse
 
 
-def _want_current(dev):
-    """The library works on the current device: tensors of another one are refused."""
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+# The calls of a serving step are short (a few us on the GPU), so their checks
+# are too: one comparison chain per tensor, the message from _want only on
+# failure, addresses and the stream handed over as plain integers.
+_BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
+
+
+def _need(t, dtype, shape, index, name):
+    """_want for a tensor of one exact shape (a tuple) on CUDA device `index`."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
+            and t.is_contiguous()):
+        _want(t, dtype, len(shape), name, shape=shape, device=torch.device("cuda", index))
+
+
+def _first(t, dtype, ndim, name):
+    """The first tensor of a call -> its device index, which has to be the
+    current device's: the library launches there."""
+    _want(t, dtype, ndim, name)
+    index = t.get_device()
+    if index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on cuda:{index}, but the current device is cuda:{torch.cuda.current_device()}")
+    return index
+
+
+_stream_of = torch._C._cuda_getCurrentRawStream  # device index -> cudaStream_t
 
 
 def attn_paged_plan(seqlens_k, seqlens_new, free_pages, block_table, page_size, max_tokens, slot_map=None,
@@ -409,40 +429,53 @@ def attn_paged_plan(seqlens_k, seqlens_new, free_pages, block_table, page_size, 
     cu_seqlens int32 [B + 1], seqlens_out int32 [B], counts int32 [2]: tokens,
     pages needed).  Tokens without a page and places behind the last token have
     slot -1."""
-    _want(seqlens_k, torch.int32, 1, "seqlens_k")
-    dev = seqlens_k.device
-    _want_current(dev)
+    dev = _first(seqlens_k, _I32, 1, "seqlens_k")
     B = seqlens_k.shape[0]
-    _want(seqlens_new, torch.int32, 1, "seqlens_new", shape=(B,), device=dev)
-    _want(free_pages, torch.int32, 1, "free_pages", device=dev)
-    _want(block_table, torch.int32, 2, "block_table", device=dev)
-    max_pages = block_table.shape[1]
-    _want(block_table, torch.int32, 2, "block_table", shape=(B, max_pages))
+    _need(seqlens_new, _I32, (B,), dev, "seqlens_new")
+    _want(free_pages, _I32, 1, "free_pages")
+    _need(free_pages, _I32, free_pages.shape, dev, "free_pages")
+    max_pages = _table_width(block_table, B, dev)
     if slot_map is None:
-        slot_map = torch.empty(max_tokens, dtype=torch.int64, device=dev)
-    _want(slot_map, torch.int64, 1, "slot_map", shape=(max_tokens,), device=dev)
+        slot_map = seqlens_k.new_empty(max_tokens, dtype=_I64)
+    else:
+        _need(slot_map, _I64, (max_tokens,), dev, "slot_map")
     if cu_seqlens is None:
-        cu_seqlens = torch.empty(B + 1, dtype=torch.int32, device=dev)
-    _want(cu_seqlens, torch.int32, 1, "cu_seqlens", shape=(B + 1,), device=dev)
+        cu_seqlens = seqlens_k.new_empty(B + 1)
+    else:
+        _need(cu_seqlens, _I32, (B + 1,), dev, "cu_seqlens")
     if seqlens_out is None:
-        seqlens_out = torch.empty(B, dtype=torch.int32, device=dev)
-    _want(seqlens_out, torch.int32, 1, "seqlens_out", shape=(B,), device=dev)
+        seqlens_out = torch.empty_like(seqlens_k)
+    else:
+        _need(seqlens_out, _I32, (B,), dev, "seqlens_out")
     if counts is None:
-        counts = torch.empty(2, dtype=torch.int32, device=dev)
-    _want(counts, torch.int32, 1, "counts", shape=(2,), device=dev)
-    _check(lib.attn_paged_plan(_ptr(seqlens_k), _ptr(seqlens_new), B, _ptr(free_pages), free_pages.shape[0],
-                               _ptr(block_table), max_pages, page_size, _ptr(slot_map), max_tokens, _ptr(cu_seqlens),
-                               _ptr(seqlens_out), _ptr(counts), _stream()), "attn_paged_plan")
+        counts = seqlens_k.new_empty(2)
+    else:
+        _need(counts, _I32, (2,), dev, "counts")
+    st = lib.attn_paged_plan(seqlens_k.data_ptr(), seqlens_new.data_ptr(), B, free_pages.data_ptr(), free_pages.shape[0],
+                             block_table.data_ptr(), max_pages, page_size, slot_map.data_ptr(), max_tokens,
+                             cu_seqlens.data_ptr(), seqlens_out.data_ptr(), counts.data_ptr(), _stream_of(dev))
+    _check(st, "attn_paged_plan")
     return slot_map, cu_seqlens, seqlens_out, counts
 
 
-def _want_cache(k_pages, v_pages, k_scales, v_scales, dev):
+def _table_width(block_table, B, dev):
+    """The int32 [B, max_pages] table's max_pages."""
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        _want(block_table, _I32, 2, "block_table")
+    max_pages = block_table.shape[1]
+    _need(block_table, _I32, (B, max_pages), dev, "block_table")
+    return max_pages
+
+
+def _cache_shape(k_pages, v_pages, k_scales, v_scales, dev):
     """The four tensors of a paged 8-bit cache -> (num_pages, page_size, Hkv, d)."""
-    _want(k_pages, torch.uint8, 4, "k_pages", device=dev)
+    _want(k_pages, _U8, 4, "k_pages")
     shape = k_pages.shape
-    _want(v_pages, torch.uint8, 4, "v_pages", shape=shape, device=dev)
-    _want(k_scales, torch.float32, 2, "k_scales", shape=(shape[0], shape[2]), device=dev)
-    _want(v_scales, torch.float32, 2, "v_scales", shape=(shape[0], shape[2]), device=dev)
+    scales = (shape[0], shape[2])
+    _need(k_pages, _U8, shape, dev, "k_pages")
+    _need(v_pages, _U8, shape, dev, "v_pages")
+    _need(k_scales, _F32, scales, dev, "k_scales")
+    _need(v_scales, _F32, scales, dev, "v_scales")
     return shape
 
 
@@ -451,11 +484,13 @@ def _want_rows(t, name, shape, dev):
     projection); the heads of a token are contiguous -> the token stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16 or t.device != dev or tuple(t.shape) != tuple(shape) or t.stride(2) != 1 \
-            or (shape[1] > 1 and t.stride(1) != shape[2]) or (shape[0] > 1 and t.stride(0) < shape[1] * shape[2]):
-        raise ValueError(f"{name}: expected bf16 rows {tuple(shape)} on {dev} with contiguous heads, got "
-                         f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
-    return t.stride(0) if shape[0] > 1 else shape[1] * shape[2]
+    tokens, H, d = shape
+    st = t.stride()
+    if t.dtype != _BF16 or t.get_device() != dev or t.shape != shape or st[2] != 1 or (H > 1 and st[1] != d) \
+            or (tokens > 1 and st[0] < H * d):
+        raise ValueError(f"{name}: expected bf16 rows {tuple(shape)} on cuda:{dev} with contiguous heads, got "
+                         f"{t.dtype} {tuple(t.shape)}, strides {st}, on {t.device}")
+    return st[0] if tokens > 1 else H * d
 
 
 def attn_append_paged_fp8(k, v, slot_map, k_pages, v_pages, k_scales, v_scales):
@@ -464,19 +499,24 @@ def attn_append_paged_fp8(k, v, slot_map, k_pages, v_pages, k_scales, v_scales):
     tokens of a longer map are taken as a slice); k_pages, v_pages: uint8 e4m3
     codes [num_pages, page_size, Hkv, d]; k_scales, v_scales: fp32
     [num_pages, Hkv]."""
-    _want(slot_map, torch.int64, 1, "slot_map")
-    dev = slot_map.device
-    _want_current(dev)
-    num_pages, page_size, H, d = _want_cache(k_pages, v_pages, k_scales, v_scales, dev)
+    dev = _first(slot_map, _I64, 1, "slot_map")
+    num_pages, page_size, H, d = _cache_shape(k_pages, v_pages, k_scales, v_scales, dev)
     tokens = slot_map.shape[0]
-    ks, vs = _want_rows(k, "k", (tokens, H, d), dev), _want_rows(v, "v", (tokens, H, d), dev)
-    _check(lib.attn_append_paged_fp8(_ptr(k), _ptr(v), ks, vs, _ptr(slot_map), tokens, _ptr(k_pages), _ptr(v_pages),
-                                     _ptr(k_scales), _ptr(v_scales), num_pages, page_size, H, d, _stream()),
-           "attn_append_paged_fp8")
+    rows = (tokens, H, d)
+    ks, vs = _want_rows(k, "k", rows, dev), _want_rows(v, "v", rows, dev)
+    st = lib.attn_append_paged_fp8(k.data_ptr(), v.data_ptr(), ks, vs, slot_map.data_ptr(), tokens, k_pages.data_ptr(),
+                                   v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), num_pages, page_size,
+                                   H, d, _stream_of(dev))
+    _check(st, "attn_append_paged_fp8")
 
 
 def attn_decode_paged_fp8_auto_splits(B, Hq, Hkv, Lk, d) -> int:
     return lib.attn_decode_paged_fp8_auto_splits(B, Hq, Hkv, Lk, d)
+
+
+def _want_heads(Hq, d, Hkv, dk):
+    if dk != d or Hkv == 0 or Hq % Hkv:
+        raise ValueError(f"k_pages: heads of {dk} elements, {Hkv} of them, do not serve {Hq} query heads of {d}")
 
 
 def attn_decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, o=None, lse=None, scale=None,
@@ -484,36 +524,36 @@ def attn_decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, 
     """Split-KV decode over a paged 8-bit cache.  q: bf16 [B,Hq,1,d]; cache as
     attn_append_paged_fp8; block_table: int32 [B, max_pages]; seqlens_k: int32
     [B], the new token included -> (o [B,Hq,1,d], lse [B,Hq])."""
-    _want(q, torch.bfloat16, 4, "q")
+    dev = _first(q, _BF16, 4, "q")
     B, Hq, Lq, d = q.shape
-    dev = q.device
-    _want_current(dev)
     if Lq != 1:
         raise ValueError(f"q: decode takes one query per head, got Lq={Lq}")
-    num_pages, page_size, Hkv, dk = _want_cache(k_pages, v_pages, k_scales, v_scales, dev)
-    if dk != d or Hkv == 0 or Hq % Hkv:
-        raise ValueError(f"k_pages: heads of {dk} elements, {Hkv} of them, do not serve {Hq} query heads of {d}")
-    _want(block_table, torch.int32, 2, "block_table", device=dev)
-    max_pages = block_table.shape[1]
-    _want(block_table, torch.int32, 2, "block_table", shape=(B, max_pages))
-    _want(seqlens_k, torch.int32, 1, "seqlens_k", shape=(B,), device=dev)
+    num_pages, page_size, Hkv, dk = _cache_shape(k_pages, v_pages, k_scales, v_scales, dev)
+    _want_heads(Hq, d, Hkv, dk)
+    max_pages = _table_width(block_table, B, dev)
+    _need(seqlens_k, _I32, (B,), dev, "seqlens_k")
     if o is None:
         o = torch.empty_like(q)
-    _want(o, torch.bfloat16, 4, "o", shape=(B, Hq, 1, d), device=dev)
+    else:
+        _need(o, _BF16, (B, Hq, 1, d), dev, "o")
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
-    _want(lse, torch.float32, 2, "lse", shape=(B, Hq), device=dev)
-    Lk = max_pages * page_size
-    S = num_splits if num_splits != 0 else attn_decode_paged_fp8_auto_splits(B, Hq, Hkv, Lk, d)
-    if workspace is None and S > 1:
-        workspace = torch.empty(attn_decode_workspace_bytes(B, Hq, Lk, d, S), dtype=torch.uint8, device=dev)
-    _want_workspace(workspace, dev)
-    scale = (1.0 / d ** 0.5) if scale is None else scale
-    _check(lib.attn_decode_paged_fp8(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales),
-                                     _ptr(block_table), max_pages, page_size, num_pages, _ptr(o), _ptr(lse),
-                                     _ptr(seqlens_k), B, Hq, Hkv, d, scale, int(window_left), S, _ptr(workspace),
-                                     0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                     _stream()), "attn_decode_paged_fp8")
+        lse = k_scales.new_empty((B, Hq))
+    else:
+        _need(lse, _F32, (B, Hq), dev, "lse")
+    if workspace is None:
+        Lk = max_pages * page_size
+        S = num_splits if num_splits != 0 else lib.attn_decode_paged_fp8_auto_splits(B, Hq, Hkv, Lk, d)
+        need = 4 * B * Hq * S * (d + 1) if S > 1 else 0  # attn_decode_workspace_bytes
+        workspace = k_pages.new_empty(need) if need > 0 else None
+    else:
+        _want_workspace(workspace, q.device)
+        need = workspace.numel() * workspace.element_size()
+    st = lib.attn_decode_paged_fp8(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+                                   v_scales.data_ptr(), block_table.data_ptr(), max_pages, page_size, num_pages,
+                                   o.data_ptr(), lse.data_ptr(), seqlens_k.data_ptr(), B, Hq, Hkv, d,
+                                   d ** -0.5 if scale is None else scale, window_left, num_splits,
+                                   None if workspace is None else workspace.data_ptr(), need, _stream_of(dev))
+    _check(st, "attn_decode_paged_fp8")
     return o, lse
 
 
@@ -527,37 +567,36 @@ def attn_fwd_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq
     new tokens of all sequences; cu_seqlens_q: int32 [B + 1]; seqlens_k: int32
     [B], the new tokens included; cache and block_table as
     attn_decode_paged_fp8 -> (o [total_q, Hq, d], lse [Hq, total_q])."""
-    _want(q, torch.bfloat16, 3, "q")
+    dev = _first(q, _BF16, 3, "q")
     total_q, Hq, d = q.shape
-    dev = q.device
-    _want_current(dev)
-    num_pages, page_size, Hkv, dk = _want_cache(k_pages, v_pages, k_scales, v_scales, dev)
-    if dk != d or Hkv == 0 or Hq % Hkv:
-        raise ValueError(f"k_pages: heads of {dk} elements, {Hkv} of them, do not serve {Hq} query heads of {d}")
-    _want(seqlens_k, torch.int32, 1, "seqlens_k", device=dev)
+    num_pages, page_size, Hkv, dk = _cache_shape(k_pages, v_pages, k_scales, v_scales, dev)
+    _want_heads(Hq, d, Hkv, dk)
+    _want(seqlens_k, _I32, 1, "seqlens_k")
     B = seqlens_k.shape[0]
-    _want(block_table, torch.int32, 2, "block_table", device=dev)
-    max_pages = block_table.shape[1]
-    _want(block_table, torch.int32, 2, "block_table", shape=(B, max_pages))
-    _want(cu_seqlens_q, torch.int32, 1, "cu_seqlens_q", shape=(B + 1,), device=dev)
+    _need(seqlens_k, _I32, (B,), dev, "seqlens_k")
+    max_pages = _table_width(block_table, B, dev)
+    _need(cu_seqlens_q, _I32, (B + 1,), dev, "cu_seqlens_q")
     if o is None:
         o = torch.empty_like(q)
-    _want(o, torch.bfloat16, 3, "o", shape=(total_q, Hq, d), device=dev)
+    else:
+        _need(o, _BF16, (total_q, Hq, d), dev, "o")
     if lse is None:
-        lse = torch.empty((Hq, total_q), dtype=torch.float32, device=dev)
-    _want(lse, torch.float32, 2, "lse", shape=(Hq, total_q), device=dev)
+        lse = k_scales.new_empty((Hq, total_q))
+    else:
+        _need(lse, _F32, (Hq, total_q), dev, "lse")
     if workspace is None:
-        need = attn_fwd_paged_fp8_workspace_bytes(B, total_q, max_seqlen_q, Hq, Hkv, max_pages * page_size, d)
-        if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _want_workspace(workspace, dev)
-    scale = (1.0 / d ** 0.5) if scale is None else scale
-    _check(lib.attn_fwd_paged_fp8(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales),
-                                  _ptr(block_table), max_pages, page_size, num_pages, _ptr(o), _ptr(lse),
-                                  _ptr(seqlens_k), _ptr(cu_seqlens_q), B, total_q, int(max_seqlen_q), Hq, Hkv, d, scale,
-                                  int(bool(causal)), int(window_left), int(window_right), _ptr(workspace),
-                                  0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                  _stream()), "attn_fwd_paged_fp8")
+        need = lib.attn_fwd_paged_fp8_workspace_bytes(B, total_q, max_seqlen_q, Hq, Hkv, max_pages * page_size, d)
+        workspace = k_pages.new_empty(need) if need > 0 else None
+    else:
+        _want_workspace(workspace, q.device)
+        need = workspace.numel() * workspace.element_size()
+    st = lib.attn_fwd_paged_fp8(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+                                v_scales.data_ptr(), block_table.data_ptr(), max_pages, page_size, num_pages,
+                                o.data_ptr(), lse.data_ptr(), seqlens_k.data_ptr(), cu_seqlens_q.data_ptr(), B, total_q,
+                                max_seqlen_q, Hq, Hkv, d, d ** -0.5 if scale is None else scale, int(bool(causal)),
+                                window_left, window_right, None if workspace is None else workspace.data_ptr(), need,
+                                _stream_of(dev))
+    _check(st, "attn_fwd_paged_fp8")
     return o, lse
 
 
