@@ -17,6 +17,7 @@
 #include "attn_bwd_sm100.cuh"
 #include "attn_fwd_f32.cuh"
 #include "attn_fwd_sm100.cuh"
+#include "attn_paged_fp8_sm100.cuh"
 #include "decode_paged_fp8.cuh"
 #include "decode_splitkv.cuh"
 #include "fp8_quant.cuh"
@@ -133,6 +134,8 @@ int device_ready(DeviceInfo* out) {
             e = e != cudaSuccess ? e : cudaFuncSetAttribute(decode_paged_fp8_kernel<128, 1, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Dp8Traits<128>::SMEM_BYTES);
             e = e != cudaSuccess ? e : cudaFuncSetAttribute(decode_paged_fp8_kernel<128, 2, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Dp8Traits<128>::SMEM_BYTES);
             e = e != cudaSuccess ? e : cudaFuncSetAttribute(decode_paged_fp8_kernel<128, 2, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Dp8Traits<128>::SMEM_BYTES);
+            e = e != cudaSuccess ? e : cudaFuncSetAttribute(attn_paged_fp8_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, ExtTraits<128>::SMEM_BYTES);
+            e = e != cudaSuccess ? e : cudaFuncSetAttribute(attn_paged_fp8_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, ExtTraits<64>::SMEM_BYTES);
             e = e != cudaSuccess ? e : cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * (PLAN_MAX_SEQ + 1) * 4);
             if (e != cudaSuccess) {
                 cudaGetLastError();

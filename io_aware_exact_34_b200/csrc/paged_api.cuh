@@ -39,6 +39,9 @@ int dp8_auto_splits(long long tiles, int Lk) {
     return static_cast<int>(S < 1 ? 1 : S);
 }
 
+// Workspace of the tensor-core kernel: its item counter.
+constexpr size_t kExtWorkspace = 16;
+
 size_t dp8_workspace(long long rows, int S, int d) {
     return S <= 1 ? 0 : static_cast<size_t>(rows) * S * (static_cast<size_t>(d) + 1) * sizeof(float);
 }
@@ -121,6 +124,72 @@ int launch_dp8(PagedFp8Params p, int d, int num_splits, void* workspace, size_t 
     }
     if (st != FATTN_OK || p.S == 1) return st;
     return d == 128 ? launch_dp8_merge<128>(p, tile_rows, s) : launch_dp8_merge<64>(p, tile_rows, s);
+}
+
+// Rows (new tokens x group heads) of a sequence from which its tiles go to the
+// tensor-core kernel.
+constexpr long long kExtMinRows = 65;
+// Its TMA coordinates are 32-bit rows of the pool.
+constexpr long long kExtMaxPoolRows = 0x7fffff00LL;
+
+bool ext_path(long long max_q, int g) { return max_q * g >= kExtMinRows; }
+
+// The pool [num_pages * page_size, Hkv, d] of codes: boxes of box_rows keys of one head.
+int encode_map_pages(CUtensorMap* map, const void* base, int d, int Hkv, long long rows, int box_rows) {
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(Hkv) * d};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(d), 1, static_cast<cuuint32_t>(box_rows)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? FATTN_OK : FATTN_ERR_CUDA;
+}
+
+// The kernel's warpgroups change their register budgets: the compiled count
+// has to provide the pool, or the raising ones would wait forever.
+template <int D>
+bool ext_register_pool_ok() {
+    cudaFuncAttributes a;
+    if (cudaFuncGetAttributes(&a, attn_paged_fp8_kernel<D>) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    using T = ExtTraits<D>;
+    return static_cast<long long>(a.numRegs) * T::THREADS >= 128LL * T::REGS_LOW + 256LL * T::REGS_HIGH;
+}
+
+int launch_ext(const PagedFp8Params& c, int d, long long pool_rows, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!workspace || workspace_bytes < kExtWorkspace) return FATTN_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return FATTN_ERR_MISALIGNED;
+    ExtParams p{};
+    p.c = c;
+    p.counter = static_cast<unsigned int*>(workspace);
+    p.toks = 128 / c.g;
+    const long long tiles = (static_cast<long long>(c.max_q) + p.toks - 1) / p.toks;
+    const long long n_items = static_cast<long long>(c.B) * c.Hkv * ((tiles + 1) / 2);
+    if (n_items > 0x7fff0000LL) return FATTN_ERR_UNSUPPORTED;
+    p.n_pairs = static_cast<int>((tiles + 1) / 2);
+    p.n_items = static_cast<int>(n_items);
+    const int page_size = 1 << c.page_shift;
+    p.box_rows = page_size < 128 ? page_size : 128;
+    DeviceInfo di;
+    int st = device_ready(&di);
+    if (st != FATTN_OK) return st;
+    if (!(d == 128 ? ext_register_pool_ok<128>() : ext_register_pool_ok<64>())) return FATTN_ERR_UNSUPPORTED;
+    CUtensorMap mk, mv;
+    if (encode_map_pages(&mk, c.k, d, c.Hkv, pool_rows, p.box_rows) != FATTN_OK ||
+        encode_map_pages(&mv, c.v, d, c.Hkv, pool_rows, p.box_rows) != FATTN_OK)
+        return FATTN_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (cudaMemsetAsync(p.counter, 0, sizeof(unsigned int), s) != cudaSuccess) {
+        cudaGetLastError();
+        return FATTN_ERR_CUDA;
+    }
+    const unsigned grid = static_cast<unsigned>(n_items < di.num_sms ? n_items : di.num_sms);
+    if (d == 128) attn_paged_fp8_kernel<128><<<grid, ExtTraits<128>::THREADS, ExtTraits<128>::SMEM_BYTES, s>>>(mk, mv, p);
+    else attn_paged_fp8_kernel<64><<<grid, ExtTraits<64>::THREADS, ExtTraits<64>::SMEM_BYTES, s>>>(mk, mv, p);
+    return cudaGetLastError() == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
 
 template <int D, int W>
@@ -252,7 +321,8 @@ int attn_decode_paged_fp8(const void* q, const void* k_pages, const void* v_page
 size_t attn_fwd_paged_fp8_workspace_bytes(int B, int total_q, int max_seqlen_q, int Hq, int Hkv, int Lk, int d) {
     if (B < 1 || total_q < 1 || max_seqlen_q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Lk < 1 || (d != 64 && d != 128))
         return 0;
-    const long long rows = static_cast<long long>(max_seqlen_q) * (Hq / Hkv);
+    const long long rows = static_cast<long long>(max_seqlen_q < total_q ? max_seqlen_q : total_q) * (Hq / Hkv);
+    if (ext_path(rows, 1)) return kExtWorkspace;
     const int t = dp8_tile_rows(rows);
     const int S = dp8_auto_splits(static_cast<long long>(B) * Hkv * ((rows + t - 1) / t), Lk);
     return dp8_workspace(static_cast<long long>(total_q) * Hq, S, d);
@@ -295,6 +365,11 @@ int attn_fwd_paged_fp8(const void* q, const void* k_pages, const void* v_pages, 
     p.window_left = window_left < 0 ? -1 : window_left;
     p.window_right = window_right < 0 ? -1 : window_right;
     p.scale_log2 = scale * 1.4426950408889634f;
+    if (ext_path(p.max_q, p.g)) {
+        const long long pool_rows = static_cast<long long>(num_pages) * page_size;
+        if (pool_rows <= kExtMaxPoolRows) return launch_ext(p, d, pool_rows, workspace, workspace_bytes, stream);
+        return launch_dp8(p, d, 1, nullptr, 0, stream);  // a pool beyond the tensor map's coordinates
+    }
     return launch_dp8(p, d, 0, workspace, workspace_bytes, stream);
 }
 
