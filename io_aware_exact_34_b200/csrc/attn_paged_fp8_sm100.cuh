@@ -426,25 +426,30 @@ __global__ void __launch_bounds__(384, 1)
                     const bool edge = ext_edge(it, j);
                     const uint32_t src = sRing + slot * T::KV_BYTES, dst = sV16 + buf * T::V16_BYTES;
                     bool nan = false;
-#pragma unroll
+#pragma unroll 1
                     for (int half = 0; half < 2; ++half) {
                         const int r = half * 64 + (warp - 2) * 32 + lane;  // key row
                         const long long key = static_cast<long long>(j) * 128 + r;
                         const bool seen = key >= it.k_lo && key < it.k_hi;
-#pragma unroll
-                        for (int c = 0; c < D / 16; ++c) {
-                            // 16 codes: chunk c of the row, exchanged by the TMA swizzle (128-byte rows: by row % 8, 64-byte
-                            // rows: by row / 2 % 4)
-                            uint4 v = lds_u4(src + r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4));
-                            if (!seen) v = make_uint4(0u, 0u, 0u, 0u);
-                            if (edge && (has_nan4(v.x) || has_nan4(v.y) || has_nan4(v.z) || has_nan4(v.w))) {
-                                nan = true;
-                                v = make_uint4(drop_nan4(v.x), drop_nan4(v.y), drop_nan4(v.z), drop_nan4(v.w));
-                            }
-                            // 32 bytes of f16: chunks 2c, 2c + 1 of 64-element (128-byte) columns of 128 rows
+                        // 16 codes: chunk c of the row, exchanged by the TMA swizzle (128-byte rows: by row % 8, 64-byte
+                        // rows: by row / 2 % 4); as f16, chunks 2c, 2c + 1 of 64-element (128-byte) columns of 128 rows
+                        auto code_at = [&](int c) { return src + r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4); };
+                        auto put = [&](int c, const uint4& v) {
                             const uint32_t row = dst + (c >> 2) * (128 * 128) + r * 128;
                             const int q = (2 * c) & 7;
                             sts_f16x16(row + ((q ^ (r & 7)) << 4), row + (((q + 1) ^ (r & 7)) << 4), v);
+                        };
+                        if (!edge) {
+#pragma unroll
+                            for (int c = 0; c < D / 16; ++c) put(c, lds_u4(code_at(c)));
+                        } else {
+#pragma unroll 1
+                            for (int c = 0; c < D / 16; ++c) {
+                                uint4 v = lds_u4(code_at(c));
+                                if (!seen) v = make_uint4(0u, 0u, 0u, 0u);
+                                nan |= has_nan4(v.x) || has_nan4(v.y) || has_nan4(v.z) || has_nan4(v.w);
+                                put(c, make_uint4(drop_nan4(v.x), drop_nan4(v.y), drop_nan4(v.z), drop_nan4(v.w)));
+                            }
                         }
                     }
                     if (nan) nan_round[round & 1] = round + 1;
