@@ -74,8 +74,9 @@ struct ExtParams {
     PagedFp8Params c;       // the cache, the rows, the mask
     unsigned int* counter;  // zeroed before the launch: the next item to deal
     int toks;               // tokens per row tile: floor(128 / g)
-    int n_pairs, n_items;   // pairs of row tiles per sequence at most; B * Hkv * n_pairs
+    int n_pairs, n_items;   // pairs of row tiles per sequence at most; B * Hkv * n_pairs * splits
     int box_rows;           // keys per TMA box: min(page_size, 128)
+    int splits;             // parts that an item's key tiles are cut into at most
 };
 
 // Instruction descriptor of kind::f16 with f16 A and B (format 0), fp32 D.
@@ -88,9 +89,13 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn, int
 // bytes), layout 4 in bits 61-63.
 constexpr uint32_t kSdescHiSw64Sbo512 = (512u >> 4) | (1u << 14) | (4u << 29);
 
-// One item: a pair of row tiles of one sequence and kv head.
+constexpr int EXT_MIN_TILES = 4;  // key tiles of the smallest part: 512 keys
+
+// One item: a pair of row tiles of one sequence and kv head, and a part of the
+// key tiles they visit.
 struct ExtItem {
     int b, h;
+    int split, active;            // this part, and the parts that hold tiles
     SeqSpan sq;
     Band band;
     int tok[2], tok_end[2];       // tokens of the tiles
@@ -98,11 +103,11 @@ struct ExtItem {
     long long k_lo, k_hi;         // keys that some row of the pair may see
 };
 
-__device__ __forceinline__ ExtItem ext_item(const ExtParams& p, int item) {
+__device__ __forceinline__ ExtItem ext_pair(const ExtParams& p, int b, int h, int pair, int split) {
     ExtItem it;
-    const int bh = item / p.n_pairs, pair = p.n_pairs - 1 - item % p.n_pairs;
-    it.b = bh / p.c.Hkv;
-    it.h = bh % p.c.Hkv;
+    it.b = b;
+    it.h = h;
+    it.split = split;
     it.sq = seq_span(p.c, it.b);
     // rows behind max_seqlen_q are not computed, but they count for the alignment
     const int n_tok = it.sq.n < p.c.max_q ? it.sq.n : p.c.max_q;
@@ -130,8 +135,36 @@ __device__ __forceinline__ ExtItem ext_item(const ExtParams& p, int item) {
             }
         }
     }
-    if (it.lo >= it.hi) it.lo = it.hi = 0;
+    it.active = 0;
+    if (it.lo >= it.hi) {
+        it.lo = it.hi = 0;
+        return it;
+    }
+    int per = (it.hi - it.lo + p.splits - 1) / p.splits;
+    per = per < EXT_MIN_TILES ? EXT_MIN_TILES : per;
+    it.active = (it.hi - it.lo + per - 1) / per;
+    if (it.active > 1) {
+        const int first = it.lo + split * per, last = first + per < it.hi ? first + per : it.hi;
+        it.lo = first < last ? first : 0;
+        it.hi = first < last ? last : 0;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            it.lo_t[t] = it.lo_t[t] > it.lo ? it.lo_t[t] : it.lo;
+            it.hi_t[t] = it.hi_t[t] < it.hi ? it.hi_t[t] : it.hi;
+            if (it.lo_t[t] >= it.hi_t[t]) it.lo_t[t] = it.hi_t[t] = 0;
+        }
+    } else if (split > 0) {
+        it.lo = it.hi = it.lo_t[0] = it.hi_t[0] = it.lo_t[1] = it.hi_t[1] = 0;
+    }
     return it;
+}
+
+// Items run through the parts of a pair, the pairs of a sequence and head from
+// the last one (the longest under causal masking), and then the heads.
+__device__ __forceinline__ ExtItem ext_item(const ExtParams& p, int item) {
+    const int split = item % p.splits, pb = item / p.splits;
+    const int bh = pb / p.n_pairs;
+    return ext_pair(p, bh / p.c.Hkv, bh % p.c.Hkv, p.n_pairs - 1 - pb % p.n_pairs, split);
 }
 
 // Whether some row of a tile that visits key tile j may not see all of it.
@@ -198,6 +231,7 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* gbase = ext_smem_raw + (base - raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.launch_dependents;");  // the merge, if there is one, may be set up
 
     const uint32_t sQ = base + T::SMEM_Q_OFF, sV16 = base + T::SMEM_V16_OFF, sRing = base + T::SMEM_RING_OFF;
     const uint32_t sScale = base + T::SMEM_SCALE_OFF;
@@ -484,9 +518,13 @@ __global__ void __launch_bounds__(384, 1)
             float* lse = p.c.lse == nullptr ? nullptr
                                             : p.c.lse + (static_cast<long long>(it.sq.q0) + tok) * p.c.lse_tok +
                                                   (static_cast<long long>(it.h) * p.c.g + head_of_row) * p.c.lse_head;
+            const bool part = it.active > 1;  // a part writes its (o, lse) to the workspace
+            const long long ws_row = q_row * p.splits + it.split;
             if (it.lo_t[t] >= it.hi_t[t]) {
                 // no key for any row of this tile
-                if (valid) {
+                if (valid && part) {
+                    if (it.split < it.active) p.c.ws_lse[ws_row] = -CUDART_INF_F;
+                } else if (valid && it.split == 0) {
                     uint4* dst = reinterpret_cast<uint4*>(p.c.o + q_row * D);
 #pragma unroll
                     for (int v = 0; v < D / 8; ++v) dst[v] = make_uint4(0u, 0u, 0u, 0u);
@@ -655,6 +693,7 @@ __global__ void __launch_bounds__(384, 1)
                 const float inv_l = empty ? 0.f : 1.f / l;
                 const bool nan = nan_round[round & 1] == round + 1;
                 __nv_bfloat16* orow = p.c.o + q_row * D;
+                float* wrow = part ? p.c.ws_o + ws_row * D : nullptr;
 #pragma unroll 1
                 for (int ch = 0; ch < D / 32; ++ch) {
                     uint32_t orr[32];
@@ -663,20 +702,32 @@ __global__ void __launch_bounds__(384, 1)
                     reg_fence(orr);
                     if (valid) {
                         const uint32_t cols = nan ? ext_nan_columns<D>(p, item, t, key_lo, key_hi, ch) : 0u;
-                        uint32_t pk16[16];
+                        float f[32];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float x0 = (cols >> (2 * e)) & 1u ? CUDART_NAN_F : __uint_as_float(orr[2 * e]) * inv_l;
-                            const float x1 = (cols >> (2 * e + 1)) & 1u ? CUDART_NAN_F : __uint_as_float(orr[2 * e + 1]) * inv_l;
-                            pk16[e] = pack_bf16x2(x0, x1);
+                        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(orr[e]) * inv_l;
+                        if (cols != 0) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if ((cols >> e) & 1u) f[e] = CUDART_NAN_F;
                         }
-                        uint4* dst = reinterpret_cast<uint4*>(orow + ch * 32);
+                        if (part) {
 #pragma unroll
-                        for (int v = 0; v < 4; ++v)
-                            dst[v] = make_uint4(pk16[4 * v], pk16[4 * v + 1], pk16[4 * v + 2], pk16[4 * v + 3]);
+                            for (int v = 0; v < 8; ++v)
+                                reinterpret_cast<float4*>(wrow + ch * 32)[v] = make_float4(f[4 * v], f[4 * v + 1], f[4 * v + 2], f[4 * v + 3]);
+                        } else {
+#pragma unroll
+                            for (int v = 0; v < 4; ++v)
+                                reinterpret_cast<uint4*>(orow + ch * 32)[v] =
+                                    make_uint4(pack_bf16x2(f[8 * v], f[8 * v + 1]), pack_bf16x2(f[8 * v + 2], f[8 * v + 3]),
+                                               pack_bf16x2(f[8 * v + 4], f[8 * v + 5]), pack_bf16x2(f[8 * v + 6], f[8 * v + 7]));
+                        }
                     }
                 }
-                if (valid && lse) *lse = empty ? -CUDART_INF_F : (my + fast_log2(l) - kDp8Shift) * 0.6931471805599453f;
+                if (valid) {
+                    const float lse2 = empty ? -CUDART_INF_F : my + fast_log2(l) - kDp8Shift;
+                    if (part) p.c.ws_lse[ws_row] = lse2;
+                    else if (lse) *lse = lse2 * 0.6931471805599453f;
+                }
                 // the next item's first product may overwrite O once this tile's P is ready, which
                 // this warp signals only after the reads above
                 tc_fence_before_sync();
@@ -705,6 +756,21 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
         tmem_dealloc(tmem, T::TMEM_COLS);
     }
+}
+
+// One row (token, query head) per warp: merge its parts.
+template <int D>
+__global__ void __launch_bounds__(128) merge_ext_kernel(const __grid_constant__ ExtParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const long long item = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    const long long per_seq = static_cast<long long>(p.c.max_q) * p.c.Hq;
+    const int b = static_cast<int>(item / per_seq), w = static_cast<int>(item % per_seq);
+    if (b >= p.c.B) return;
+    const int i = w / p.c.Hq, hq = w % p.c.Hq;
+    const SeqSpan sq = seq_span(p.c, b);
+    if (i >= (sq.n < p.c.max_q ? sq.n : p.c.max_q)) return;
+    const ExtItem it = ext_pair(p, b, hq / p.c.g, i / p.toks / 2, 0);
+    if (it.active > 1) merge_row<D>(p.c, sq, i, hq, it.active, p.splits);
 }
 
 }  // namespace fattn

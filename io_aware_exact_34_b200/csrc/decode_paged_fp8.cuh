@@ -628,32 +628,17 @@ __global__ void __launch_bounds__(32 * DP8_WARPS) decode_paged_fp8_kernel(const 
     }
 }
 
-// One row (token, query head) per warp: merge its splits.  grid.x = rows of
-// one sequence and head group in tiles of 4, as the split kernel cut them.
+// One warp: the row of token i and query head hq of a sequence from its
+// `active` partial (o, lse) pairs, `stride` of them to a row in the workspace.
 template <int D>
-__global__ void __launch_bounds__(128) merge_paged_fp8_kernel(const PagedFp8Params p, int tile_rows) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+__device__ __forceinline__ void merge_row(const PagedFp8Params& p, const SeqSpan& sq, int i, int hq, int active, int stride) {
     constexpr int EPL = D / 32;  // elements per lane
     const int lane = threadIdx.x & 31;
-    const long long item = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const int per_seq = p.max_q * p.Hq;
-    const int b = static_cast<int>(item / per_seq), w = static_cast<int>(item % per_seq);
-    if (b >= p.B) return;
-    const SeqSpan sq = seq_span(p, b);
-    const int i = w / p.Hq, hq = w % p.Hq;
-    const int n_tok = sq.n < p.max_q ? sq.n : p.max_q;
-    if (i >= n_tok) return;
-    // the tile of this row, whose union of keys was split
-    const int row = i * p.g + hq % p.g;
-    const int row0 = row / tile_rows * tile_rows;
-    const int rows = n_tok * p.g - row0 < tile_rows ? n_tok * p.g - row0 : tile_rows;
-    const SplitSpan sp = split_span(p, sq, row0 / p.g, (row0 + rows - 1) / p.g, 0);
-    if (sp.active <= 1) return;  // written by the split kernel
     const long long r = (static_cast<long long>(sq.q0) + i) * p.Hq + hq;
-    const float* ls = p.ws_lse + r * p.S;
+    const float* ls = p.ws_lse + r * stride;
     float M = -CUDART_INF_F;
     bool nan = false;
-    for (int s = lane; s < sp.active; s += 32) {
+    for (int s = lane; s < active; s += 32) {
         const float x = ls[s];
         nan |= x != x;
         M = fmaxf(M, x);
@@ -666,10 +651,12 @@ __global__ void __launch_bounds__(128) merge_paged_fp8_kernel(const PagedFp8Para
 #pragma unroll
     for (int e = 0; e < EPL; ++e) f[e] = 0.f;
 #pragma unroll 4
-    for (int s = 0; s < sp.active; ++s) {
-        const float wt = fast_exp2(ls[s] - safe);
+    for (int s = 0; s < active; ++s) {
+        const float x = ls[s];
+        if (x == -CUDART_INF_F) continue;  // no key of this row: its o may not have been written
+        const float wt = fast_exp2(x - safe);
         W += wt;
-        const float* src = p.ws_o + (r * p.S + s) * D + lane * EPL;
+        const float* src = p.ws_o + (r * stride + s) * D + lane * EPL;
         if constexpr (EPL == 4) {
             const float4 v = *reinterpret_cast<const float4*>(src);
             f[0] = fmaf(wt, v.x, f[0]), f[1] = fmaf(wt, v.y, f[1]), f[2] = fmaf(wt, v.z, f[2]), f[3] = fmaf(wt, v.w, f[3]);
@@ -686,6 +673,26 @@ __global__ void __launch_bounds__(128) merge_paged_fp8_kernel(const PagedFp8Para
     if (lane == 0 && p.lse != nullptr)
         p.lse[(static_cast<long long>(sq.q0) + i) * p.lse_tok + static_cast<long long>(hq) * p.lse_head] =
             empty ? -CUDART_INF_F : (M + fast_log2(W)) * 0.6931471805599453f;
+}
+
+// One row (token, query head) per warp: merge its splits.
+template <int D>
+__global__ void __launch_bounds__(128) merge_paged_fp8_kernel(const PagedFp8Params p, int tile_rows) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const long long item = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    const long long per_seq = static_cast<long long>(p.max_q) * p.Hq;
+    const int b = static_cast<int>(item / per_seq), w = static_cast<int>(item % per_seq);
+    if (b >= p.B) return;
+    const SeqSpan sq = seq_span(p, b);
+    const int i = w / p.Hq, hq = w % p.Hq;
+    const int n_tok = sq.n < p.max_q ? sq.n : p.max_q;
+    if (i >= n_tok) return;
+    // the tile of this row, whose union of keys was split
+    const int row = i * p.g + hq % p.g;
+    const int row0 = row / tile_rows * tile_rows;
+    const int rows = n_tok * p.g - row0 < tile_rows ? n_tok * p.g - row0 : tile_rows;
+    const SplitSpan sp = split_span(p, sq, row0 / p.g, (row0 + rows - 1) / p.g, 0);
+    if (sp.active > 1) merge_row<D>(p, sq, i, hq, sp.active, p.S);  // else written by the split kernel
 }
 
 }  // namespace fattn

@@ -39,9 +39,6 @@ int dp8_auto_splits(long long tiles, int Lk) {
     return static_cast<int>(S < 1 ? 1 : S);
 }
 
-// Workspace of the tensor-core kernel: its item counter.
-constexpr size_t kExtWorkspace = 16;
-
 size_t dp8_workspace(long long rows, int S, int d) {
     return S <= 1 ? 0 : static_cast<size_t>(rows) * S * (static_cast<size_t>(d) + 1) * sizeof(float);
 }
@@ -52,11 +49,11 @@ int launch_dp8_kernel(const PagedFp8Params& p, unsigned grid, cudaStream_t s) {
     return cudaGetLastError() == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
 
-template <int D>
-int launch_dp8_merge(const PagedFp8Params& p, int tile_rows, cudaStream_t s) {
+// A merge kernel of one warp per row, set up while the kernel before it runs.
+template <typename... Args>
+int launch_merge(void (*kernel)(Args...), long long rows, cudaStream_t s, Args... args) {
     cudaLaunchConfig_t cfg{};
-    const long long items = static_cast<long long>(p.B) * p.max_q * p.Hq;
-    cfg.gridDim = dim3(static_cast<unsigned>((items + 3) / 4));
+    cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4));
     cfg.blockDim = dim3(128);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -64,7 +61,7 @@ int launch_dp8_merge(const PagedFp8Params& p, int tile_rows, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, merge_paged_fp8_kernel<D>, p, tile_rows) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
         cudaGetLastError();
         return FATTN_ERR_CUDA;
     }
@@ -123,7 +120,9 @@ int launch_dp8(PagedFp8Params p, int d, int num_splits, void* workspace, size_t 
         else st = masked ? launch_dp8_kernel<64, 2, true>(p, grid, s) : launch_dp8_kernel<64, 2, false>(p, grid, s);
     }
     if (st != FATTN_OK || p.S == 1) return st;
-    return d == 128 ? launch_dp8_merge<128>(p, tile_rows, s) : launch_dp8_merge<64>(p, tile_rows, s);
+    const long long all = static_cast<long long>(p.B) * p.max_q * p.Hq;
+    return d == 128 ? launch_merge(merge_paged_fp8_kernel<128>, all, s, p, tile_rows)
+                    : launch_merge(merge_paged_fp8_kernel<64>, all, s, p, tile_rows);
 }
 
 // Rows (new tokens x group heads) of a sequence from which its tiles go to the
@@ -133,6 +132,29 @@ constexpr long long kExtMinRows = 65;
 constexpr long long kExtMaxPoolRows = 0x7fffff00LL;
 
 bool ext_path(long long max_q, int g) { return max_q * g >= kExtMinRows; }
+
+// Pairs of row tiles of one sequence.
+long long ext_pairs(long long max_q, int g) {
+    const long long toks = 128 / g;
+    return ((max_q + toks - 1) / toks + 1) / 2;
+}
+
+#ifndef EXT_TARGET
+#define EXT_TARGET 444
+#endif
+// Parts of an item's key tiles: enough that the items fill 148 SMs three times
+// over, at least EXT_MIN_TILES tiles to a part.
+int ext_splits(long long items, int Lk) {
+    long long S = (EXT_TARGET + items - 1) / items;
+    const long long most = (static_cast<long long>(Lk) + 128 * EXT_MIN_TILES - 1) / (128 * EXT_MIN_TILES);
+    S = S > 32 ? 32 : S;
+    S = S > most ? most : S;
+    return static_cast<int>(S < 1 ? 1 : S);
+}
+
+// The item counter, then the parts' (o, lse).
+constexpr size_t kExtCounterBytes = 16;
+size_t ext_workspace(long long rows, int S, int d) { return kExtCounterBytes + dp8_workspace(rows, S, d); }
 
 // The pool [num_pages * page_size, Hkv, d] of codes: boxes of box_rows keys of one head.
 int encode_map_pages(CUtensorMap* map, const void* base, int d, int Hkv, long long rows, int box_rows) {
@@ -160,16 +182,19 @@ bool ext_register_pool_ok() {
 }
 
 int launch_ext(const PagedFp8Params& c, int d, long long pool_rows, void* workspace, size_t workspace_bytes, void* stream) {
-    if (!workspace || workspace_bytes < kExtWorkspace) return FATTN_ERR_WORKSPACE;
-    if (!aligned16(workspace)) return FATTN_ERR_MISALIGNED;
     ExtParams p{};
     p.c = c;
-    p.counter = static_cast<unsigned int*>(workspace);
     p.toks = 128 / c.g;
-    const long long tiles = (static_cast<long long>(c.max_q) + p.toks - 1) / p.toks;
-    const long long n_items = static_cast<long long>(c.B) * c.Hkv * ((tiles + 1) / 2);
-    if (n_items > 0x7fff0000LL) return FATTN_ERR_UNSUPPORTED;
-    p.n_pairs = static_cast<int>((tiles + 1) / 2);
+    p.n_pairs = static_cast<int>(ext_pairs(c.max_q, c.g));
+    const long long items = static_cast<long long>(c.B) * c.Hkv * p.n_pairs;
+    p.splits = ext_splits(items, c.max_pages << c.page_shift);
+    const long long n_items = items * p.splits, rows = static_cast<long long>(c.total_q) * c.Hq;
+    if (n_items > 0x7fff0000LL || static_cast<long long>(c.B) * c.max_q * c.Hq > 0x7fffffffLL) return FATTN_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < ext_workspace(rows, p.splits, d)) return FATTN_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return FATTN_ERR_MISALIGNED;
+    p.counter = static_cast<unsigned int*>(workspace);
+    p.c.ws_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + kExtCounterBytes);
+    p.c.ws_lse = p.c.ws_o + rows * p.splits * d;
     p.n_items = static_cast<int>(n_items);
     const int page_size = 1 << c.page_shift;
     p.box_rows = page_size < 128 ? page_size : 128;
@@ -189,15 +214,17 @@ int launch_ext(const PagedFp8Params& c, int d, long long pool_rows, void* worksp
     const unsigned grid = static_cast<unsigned>(n_items < di.num_sms ? n_items : di.num_sms);
     if (d == 128) attn_paged_fp8_kernel<128><<<grid, ExtTraits<128>::THREADS, ExtTraits<128>::SMEM_BYTES, s>>>(mk, mv, p);
     else attn_paged_fp8_kernel<64><<<grid, ExtTraits<64>::THREADS, ExtTraits<64>::SMEM_BYTES, s>>>(mk, mv, p);
-    return cudaGetLastError() == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+    if (cudaGetLastError() != cudaSuccess) return FATTN_ERR_CUDA;
+    if (p.splits == 1) return FATTN_OK;
+    const long long all = static_cast<long long>(c.B) * c.max_q * c.Hq;
+    return d == 128 ? launch_merge(merge_ext_kernel<128>, all, s, p) : launch_merge(merge_ext_kernel<64>, all, s, p);
 }
 
-template <int D, int W>
+template <int D, int WARPS>
 int launch_append(const AppendParams& p, cudaStream_t s) {
-    constexpr int UNITS = W == 1 ? 4 : 1;
-    const long long grid = (p.units + UNITS - 1) / UNITS;
+    const long long grid = (static_cast<long long>(p.T) + p.chunk - 1) / p.chunk * p.H * 2;
     if (grid > 0x7fffffffLL) return FATTN_ERR_UNSUPPORTED;
-    append_paged_fp8_kernel<D, W><<<static_cast<unsigned>(grid), W == 1 ? 128 : 32 * W, 0, s>>>(p);
+    append_paged_fp8_kernel<D, WARPS><<<static_cast<unsigned>(grid), 32 * WARPS, 0, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
 
@@ -264,15 +291,15 @@ int attn_append_paged_fp8(const void* k, const void* v, long long k_stride, long
     p.T = num_tokens;
     p.H = H;
     p.page_shift = log2_of(page_size);
-    // warps to a unit so that a page's rows stay in its registers; tokens to a
-    // unit so that the units are about one wave of 64 warps an SM
-    const int W = page_size <= 16 ? 1 : (page_size <= 64 ? 4 : 8);
+    // a warp for every 16 rows of a page; tokens to a CTA so that the warps are
+    // about one wave of 64 an SM
+    const int W = page_size >= 128 ? 8 : page_size / 16;
     long long chunk = (2LL * H * num_tokens * W + 64LL * di.num_sms - 1) / (64LL * di.num_sms);
-    p.chunk = static_cast<int>(chunk < 1 ? 1 : (chunk > 16 ? 16 : chunk));
-    p.units = (static_cast<long long>(num_tokens) + p.chunk - 1) / p.chunk * H * 2;
+    p.chunk = static_cast<int>(chunk < 1 ? 1 : (chunk > 32 ? 32 : chunk));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (d == 128) return W == 1 ? launch_append<128, 1>(p, s) : (W == 4 ? launch_append<128, 4>(p, s) : launch_append<128, 8>(p, s));
-    return W == 1 ? launch_append<64, 1>(p, s) : (W == 4 ? launch_append<64, 4>(p, s) : launch_append<64, 8>(p, s));
+    if (d == 128)
+        return W == 1 ? launch_append<128, 1>(p, s) : W == 2 ? launch_append<128, 2>(p, s) : W == 4 ? launch_append<128, 4>(p, s) : launch_append<128, 8>(p, s);
+    return W == 1 ? launch_append<64, 1>(p, s) : W == 2 ? launch_append<64, 2>(p, s) : W == 4 ? launch_append<64, 4>(p, s) : launch_append<64, 8>(p, s);
 }
 
 int attn_decode_paged_fp8_auto_splits(int B, int Hq, int Hkv, int Lk, int d) {
@@ -321,11 +348,14 @@ int attn_decode_paged_fp8(const void* q, const void* k_pages, const void* v_page
 size_t attn_fwd_paged_fp8_workspace_bytes(int B, int total_q, int max_seqlen_q, int Hq, int Hkv, int Lk, int d) {
     if (B < 1 || total_q < 1 || max_seqlen_q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Lk < 1 || (d != 64 && d != 128))
         return 0;
-    const long long rows = static_cast<long long>(max_seqlen_q < total_q ? max_seqlen_q : total_q) * (Hq / Hkv);
-    if (ext_path(rows, 1)) return kExtWorkspace;
+    const long long max_q = max_seqlen_q < total_q ? max_seqlen_q : total_q;
+    const int g = Hq / Hkv;
+    const long long rows = max_q * g, all = static_cast<long long>(total_q) * Hq;
+    if (g <= 128 && ext_path(max_q, g))
+        return ext_workspace(all, ext_splits(static_cast<long long>(B) * Hkv * ext_pairs(max_q, g), Lk), d);
     const int t = dp8_tile_rows(rows);
     const int S = dp8_auto_splits(static_cast<long long>(B) * Hkv * ((rows + t - 1) / t), Lk);
-    return dp8_workspace(static_cast<long long>(total_q) * Hq, S, d);
+    return dp8_workspace(all, S, d);
 }
 
 int attn_fwd_paged_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,

@@ -10,14 +10,15 @@
 // half a subnormal step, 2^-10 of the scale.
 //
 // Work split.  A run is a maximal stretch of consecutive tokens whose slots
-// lie in one page.  One unit of W warps takes a run of one head of K or V:
-// the largest finite |x| of the new rows, the scale, the old rows if the
-// scale grew, the new rows.  New rows are read once and stay in registers (up
-// to 16 * W rows at d = 128; longer runs read the rest again from L2).  W goes
-// by the page size, so that a full page's rows are held by their unit.  A unit
-// looks for the starts of its runs among `chunk` tokens; chunk is 1 while
-// there are too few units to fill the GPU (a decode step) and grows to 16 (a
-// prefill, where most tokens start no run).
+// lie in one page; of every run and head the work is: the largest finite |x| of
+// the new rows, the scale, the old rows if the scale grew, the new rows.  A CTA
+// takes `chunk` tokens of one head of K or V and the runs that start there.
+// It has a warp for every 16 rows of a page (1 to 8): where its runs are long
+// they share the rows of one run after the other, where there are as many runs
+// as warps (decode steps) each warp takes runs of its own.  The first 16 rows of
+// a warp (d = 128) stay in registers between the two passes, the rest is read
+// again from L2.  chunk grows from 1 (a decode step, too few tokens to fill the
+// GPU) to 32 (a prefill, where most tokens start no run).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -35,7 +36,6 @@ struct AppendParams {
     const long long* slots;     // [T]
     long long num_slots;        // num_pages * page_size
     int T, H, page_shift, chunk;
-    long long units;
 };
 
 constexpr int kMinScaleExp = -60;
@@ -88,21 +88,17 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float ratio) {
     return pack_e4m3x4(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
 }
 
-template <int D, int W>
-__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) append_paged_fp8_kernel(const AppendParams p) {
-    constexpr int UNITS = W == 1 ? 4 : 1;  // units per CTA
-    constexpr int LPR = D / 8;             // lanes per row, 8 elements each
-    constexpr int RPS = 32 / LPR;          // rows per warp step
-    constexpr int HOLD = 8;                // steps held in registers
-    __shared__ uint32_t sm_amax[W];
-    const int lane = threadIdx.x & 31;
-    const int wu = W == 1 ? 0 : threadIdx.x >> 5;  // warp of the unit
-    const long long unit = static_cast<long long>(blockIdx.x) * UNITS + (W == 1 ? threadIdx.x >> 5 : 0);
-    if (unit >= p.units) return;  // the whole unit
-    const int kv = static_cast<int>(unit % 2);
-    const long long u2 = unit / 2;
-    const int h = static_cast<int>(u2 % p.H);
-    const long long t_lo = (u2 / p.H) * p.chunk;
+template <int D, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) append_paged_fp8_kernel(const AppendParams p) {
+    constexpr int LPR = D / 8;   // lanes per row, 8 elements each
+    constexpr int RPS = 32 / LPR;  // rows per warp step
+    constexpr int HOLD = 8;      // steps held in registers
+    __shared__ uint32_t sm_amax[WARPS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // CTA = (chunk of tokens, head, K or V), K and V fastest
+    const int kv = blockIdx.x & 1;
+    const int h = (blockIdx.x >> 1) % p.H;
+    const long long t_lo = static_cast<long long>((blockIdx.x >> 1) / p.H) * p.chunk;
     const long long t_hi = t_lo + p.chunk < p.T ? t_lo + p.chunk : p.T;
     const int shift = p.page_shift;
     const long long page_mask = (1LL << shift) - 1;
@@ -117,52 +113,57 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) append_paged_fp8_kernel
         const long long s = __ldg(p.slots + t);
         return s >= 0 && s < p.num_slots ? s >> shift : -1;
     };
-    for (long long t = t_lo; t < t_hi;) {
+
+    // One run of tokens from t on, by `warps` warps of which this one is `w`.
+    auto do_run = [&](long long t, int w, int warps) {
         const long long page = page_of(t);
-        const bool start = page >= 0 && (t == 0 || page_of(t - 1) != page);
-        if (!start) {
-            ++t;
-            continue;
-        }
         // the run's end, its lowest row, and whether its slots rise by one
         long long n = 0;
         int first = 0x7fffffff;
         bool dense = true;
-        for (;;) {
-            const long long i = t + n + lane;
-            long long s = -1;
-            if (i < p.T && page_of(i) == page) s = __ldg(p.slots + i);
-            const unsigned in = __ballot_sync(0xffffffffu, s >= 0);
-            const int m = in == 0xffffffffu ? 32 : __ffs(~in) - 1;
-            int off = lane < m ? static_cast<int>(s & page_mask) : 0x7fffffff;
-            if (lane < m && n + lane > 0 && s != __ldg(p.slots + i - 1) + 1) dense = false;
+        long long before = 0;  // the slot of the token before the 32 in hand
+        for (bool more = true; more;) {
+            constexpr int AHEAD = 4;  // loads in flight: 128 tokens
+            long long s[AHEAD];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const int y = __shfl_xor_sync(0xffffffffu, off, o);
-                off = y < off ? y : off;
+            for (int k = 0; k < AHEAD; ++k) {
+                const long long i = t + n + 32 * k + lane;
+                s[k] = i < p.T ? __ldg(p.slots + i) : -1;
             }
-            first = off < first ? off : first;
-            n += m;
-            if (m < 32) break;
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                if (!more) break;
+                const unsigned in = __ballot_sync(0xffffffffu, s[k] >= 0 && s[k] < p.num_slots && (s[k] >> shift) == page);
+                const int m = in == 0xffffffffu ? 32 : __ffs(~in) - 1;
+                const int off = lane < m ? static_cast<int>(s[k] & page_mask) : 0x7fffffff;
+                long long prev = __shfl_up_sync(0xffffffffu, s[k], 1);
+                if (lane == 0) prev = n == 0 ? s[k] - 1 : before;
+                if (lane < m && s[k] != prev + 1) dense = false;
+                const int low = __reduce_min_sync(0xffffffffu, off);
+                first = low < first ? low : first;
+                before = __shfl_sync(0xffffffffu, s[k], 31);
+                n += m;
+                more = m == 32;
+            }
         }
         dense = __all_sync(0xffffffffu, dense);
 
-        const long long r0 = wu * RPS + lane / LPR;  // this lane's row in step 0
-        constexpr long long RSTEP = static_cast<long long>(W) * RPS;
+        const long long r0 = w * RPS + lane / LPR;  // this lane's row in step 0
+        const long long rstep = static_cast<long long>(warps) * RPS;
         uint4 hold[HOLD];
         uint32_t amax = 0;  // the largest finite magnitude, as bf16 bits
         auto take = [&](const uint4& v) {
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                uint32_t a = w[e] & 0x7FFF7FFFu;
+                uint32_t a = u[e] & 0x7FFF7FFFu;
                 a &= ~__vcmpgeu2(a, 0x7F807F80u);
                 amax = __vmaxu2(amax, a);
             }
         };
 #pragma unroll
         for (int i = 0; i < HOLD; ++i) {
-            const long long r = r0 + i * RSTEP;
+            const long long r = r0 + i * rstep;
             hold[i] = make_uint4(0u, 0u, 0u, 0u);
             if (r < n) hold[i] = __ldg(reinterpret_cast<const uint4*>(x + (t + r) * stride));
         }
@@ -170,48 +171,62 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) append_paged_fp8_kernel
         const float s_old = first > 0 ? scales[page * p.H] : 0.f;
 #pragma unroll
         for (int i = 0; i < HOLD; ++i) take(hold[i]);
-        for (long long r = r0 + HOLD * RSTEP; r < n; r += RSTEP)
+        for (long long r = r0 + HOLD * rstep; r < n; r += rstep)
             take(__ldg(reinterpret_cast<const uint4*>(x + (t + r) * stride)));
         amax = __vmaxu2(amax, amax >> 16) & 0xFFFFu;
         amax = __reduce_max_sync(0xffffffffu, amax);
-        if constexpr (W > 1) {
+        if (WARPS > 1 && warps > 1) {
             __syncthreads();  // the previous run's reads of sm_amax
-            if (lane == 0) sm_amax[wu] = amax;
+            if (lane == 0) sm_amax[warp] = amax;
             __syncthreads();
 #pragma unroll
-            for (int w = 0; w < W; ++w) amax = sm_amax[w] > amax ? sm_amax[w] : amax;
+            for (int k = 0; k < WARPS; ++k) amax = sm_amax[k] > amax ? sm_amax[k] : amax;
         } else {
             __syncwarp();
         }
         const float s = fmaxf(s_old, pow2_scale(amax << 16));
         const float inv = __frcp_rn(s);
-        if (wu == 0 && lane == 0) scales[page * p.H] = s;
+        if (w == 0 && lane == 0) scales[page * p.H] = s;
         uint8_t* page_rows = pages + (page << shift) * row_bytes;
         if (first > 0 && s != s_old) {
             const float ratio = s_old * inv;
-            for (long long r = r0; r < first; r += RSTEP) {
+            for (long long r = r0; r < first; r += rstep) {
                 uint2* q = reinterpret_cast<uint2*>(page_rows + r * row_bytes);
                 const uint2 c = *q;
                 *q = make_uint2(rescale4(c.x, ratio), rescale4(c.y, ratio));
             }
         }
         auto put = [&](long long r, const uint4& v) {
-            const long long slot = __ldg(p.slots + t + r);
+            long long at = first + r;
             if (!dense) {
                 // a slot named again by a later token of the run keeps that token's row
+                const long long slot = __ldg(p.slots + t + r);
                 for (long long i = r + 1; i < n; ++i)
                     if (__ldg(p.slots + t + i) == slot) return;
+                at = slot & page_mask;
             }
-            *reinterpret_cast<uint2*>(page_rows + (slot & page_mask) * row_bytes) = quantize8(v, inv);
+            *reinterpret_cast<uint2*>(page_rows + at * row_bytes) = quantize8(v, inv);
         };
 #pragma unroll
         for (int i = 0; i < HOLD; ++i) {
-            const long long r = r0 + i * RSTEP;
+            const long long r = r0 + i * rstep;
             if (r < n) put(r, hold[i]);
         }
-        for (long long r = r0 + HOLD * RSTEP; r < n; r += RSTEP)
+        for (long long r = r0 + HOLD * rstep; r < n; r += rstep)
             put(r, __ldg(reinterpret_cast<const uint4*>(x + (t + r) * stride)));
-        t += n;
+    };
+
+    // the tokens of the chunk that start a run (the same in every warp)
+    bool start = false;
+    if (t_lo + lane < t_hi) {
+        const long long page = page_of(t_lo + lane);
+        start = page >= 0 && (t_lo + lane == 0 || page_of(t_lo + lane - 1) != page);
+    }
+    unsigned starts = __ballot_sync(0xffffffffu, start);
+    const bool own = __popc(starts) >= WARPS;
+    for (int k = 0; starts != 0; starts &= starts - 1, ++k) {
+        if (own && k % WARPS != warp) continue;
+        do_run(t_lo + __ffs(starts) - 1, own ? 0 : warp, own ? 1 : WARPS);
     }
 }
 

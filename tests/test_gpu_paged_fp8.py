@@ -402,6 +402,10 @@ FWD_CASES = [
     ([20, 0, 3], [50, 7, 3], 16, 4, 2, 128, {}), ([20, 5], [50, 9], 16, 2, 1, 64, dict(left=3)), ([5], [300], 16, 4, 1, 128, dict(causal=False, right=2)),
     ([600, 80], [256, 80], 128, 16, 4, 128, dict(behind=5)), ([600, 80], [256, 20], 16, 4, 2, 128, dict(most=33)),
     ([900], [300], 16, 4, 2, 128, dict(spread=20)),
+    # keys in several parts, some of them without a key for some rows
+    ([3000, 700, 5], [100, 64, 5], 16, 8, 2, 128, {}), ([2500], [40], 64, 8, 1, 64, dict(left=900)),
+    ([2100, 1300], [70, 70], 32, 4, 4, 128, dict(causal=False)), ([2600], [33], 16, 16, 4, 64, dict(causal=False, left=700, right=300)),
+    ([4200], [1400], 256, 2, 1, 128, dict(left=300)), ([1030, 40], [1030, 600], 128, 2, 2, 64, {}),
 ]
 
 
@@ -415,6 +419,12 @@ def test_fwd_nan_values_spare_rows_that_do_not_see_them(fl, hq, hkv, d, new):
     """A NaN in V reaches its column in the rows that see its key, and no other row."""
     _fwd_case(fl, [300, 220], [new, 1], 16, hq, hkv, d, seed=3, nan_v=[(0, 298, hkv - 1, 5), (0, 300 - new, 0, 0), (1, 219, 0, d - 1)])
     _fwd_case(fl, [300], [new], 16, hq, hkv, d, seed=4, left=40, nan_v=[(0, 290, 0, 1), (0, 300 - new - 20, hkv - 1, 2)])
+
+
+def test_fwd_nan_values_in_parts(fl):
+    """The same where the keys are cut into parts."""
+    _fwd_case(fl, [2900], [90], 16, 4, 2, 128, seed=5, nan_v=[(0, 2890, 0, 5), (0, 2830, 1, 0), (0, 2899, 1, 127)])
+    _fwd_case(fl, [2900], [90], 32, 4, 1, 64, seed=6, left=1500, nan_v=[(0, 2895, 0, 5), (0, 1330, 0, 0), (0, 1400, 0, 63)])
 
 
 def test_fwd_one_token_is_decode(fl):
