@@ -61,7 +61,8 @@ struct ExtTraits {
     // sc_full, sc_empty[SCALE_SLOTS]; drain
     static constexpr int NBAR = 2 * NSTAGE + 16 + 2 * SCALE_SLOTS + 1;
     static constexpr int SMEM_MISC_OFF = SMEM_BAR_OFF + NBAR * 8;
-    // misc words: TMEM address, abort flag, items[2], NaN rounds[2]
+    // misc words: TMEM address, abort flag, items[2], NaN rounds[4] (an item is dealt once every
+    // role has read the item two rounds before it, so a round's entry outlives its epilogue)
     static constexpr int SMEM_BYTES = SMEM_MISC_OFF + 32 + 1024;  // + alignment slack
     static_assert(SMEM_BYTES <= 232448, "shared memory");
     // Register split as attn_fwd_sm100.cuh: 128 * 80 + 256 * 208 = 63488 <= 384 * 168.
@@ -96,42 +97,56 @@ constexpr int EXT_MIN_TILES = 4;  // key tiles of the smallest part: 512 keys
 struct ExtItem {
     int b, h;
     int split, active;            // this part, and the parts that hold tiles
-    SeqSpan sq;
-    Band band;
+    int q0, n, len;               // first token, tokens and keys of the sequence
     int tok[2], tok_end[2];       // tokens of the tiles
     int lo_t[2], hi_t[2], lo, hi; // their key tiles, and the union
-    long long k_lo, k_hi;         // keys that some row of the pair may see
+    int full_lo[2], full_hi[2];   // keys every row of a tile may see
+    int k_lo, k_hi;               // keys that some row of the pair may see
 };
+
+// Keys [lo, hi) of token i, as key_range.
+__device__ __forceinline__ void ext_keys(const PagedFp8Params& c, int n, int len, int i, int* lo, int* hi) {
+    const int pos = i + (len - n);
+    const long long right = c.causal ? 0 : c.window_right;
+    int h = len, l = 0;
+    if (right >= 0 && pos + right + 1 < h) h = static_cast<int>(pos + right + 1);
+    if (c.window_left >= 0 && pos > c.window_left) l = pos - c.window_left;
+    *lo = l;
+    *hi = h > l ? h : l;
+}
 
 __device__ __forceinline__ ExtItem ext_pair(const ExtParams& p, int b, int h, int pair, int split) {
     ExtItem it;
     it.b = b;
     it.h = h;
     it.split = split;
-    it.sq = seq_span(p.c, it.b);
+    const SeqSpan sq = seq_span(p.c, b);
+    it.q0 = sq.q0;
+    it.n = sq.n;
+    it.len = static_cast<int>(sq.len);
     // rows behind max_seqlen_q are not computed, but they count for the alignment
-    const int n_tok = it.sq.n < p.c.max_q ? it.sq.n : p.c.max_q;
-    it.band = make_band(it.sq.n, it.sq.len, p.c.causal, p.c.window_left, p.c.window_right);
-    it.lo = 0x7fffffff;
-    it.hi = 0;
-    it.k_lo = 0x7fffffffLL;
-    it.k_hi = 0;
+    const int n_tok = it.n < p.c.max_q ? it.n : p.c.max_q;
+    it.lo = it.k_lo = 0x7fffffff;
+    it.hi = it.k_hi = 0;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         const long long first = static_cast<long long>(2 * pair + t) * p.toks;
         it.tok[t] = first < n_tok ? static_cast<int>(first) : n_tok;
         it.tok_end[t] = first + p.toks < n_tok ? static_cast<int>(first + p.toks) : n_tok;
-        it.lo_t[t] = it.hi_t[t] = 0;
-        if (it.tok[t] < it.tok_end[t] && it.sq.len > 0) {
-            kv_tile_range(it.band, it.tok[t], it.tok_end[t] - 1, 128, &it.lo_t[t], &it.hi_t[t]);
-            if (it.lo_t[t] < it.hi_t[t]) {
+        it.lo_t[t] = it.hi_t[t] = it.full_lo[t] = it.full_hi[t] = 0;
+        if (it.tok[t] < it.tok_end[t]) {
+            int lo0, hi0, lo1, hi1;  // of the first and the last token: both ends rise with the token
+            ext_keys(p.c, it.n, it.len, it.tok[t], &lo0, &hi0);
+            ext_keys(p.c, it.n, it.len, it.tok_end[t] - 1, &lo1, &hi1);
+            it.full_lo[t] = lo1;
+            it.full_hi[t] = hi0;
+            if (lo0 < hi1) {
+                it.lo_t[t] = lo0 >> 7;
+                it.hi_t[t] = (hi1 + 127) >> 7;
                 it.lo = it.lo_t[t] < it.lo ? it.lo_t[t] : it.lo;
                 it.hi = it.hi_t[t] > it.hi ? it.hi_t[t] : it.hi;
-                long long a, e;
-                key_range(p.c, it.sq, it.tok[t], &a, &e);
-                it.k_lo = a < it.k_lo ? a : it.k_lo;
-                key_range(p.c, it.sq, it.tok_end[t] - 1, &a, &e);
-                it.k_hi = e > it.k_hi ? e : it.k_hi;
+                it.k_lo = lo0 < it.k_lo ? lo0 : it.k_lo;
+                it.k_hi = hi1 > it.k_hi ? hi1 : it.k_hi;
             }
         }
     }
@@ -172,8 +187,7 @@ __device__ __forceinline__ bool ext_edge(const ExtItem& it, int j) {
     bool edge = false;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
-        if (j >= it.lo_t[t] && j < it.hi_t[t])
-            edge |= !tile_is_full(it.band, it.tok[t], it.tok_end[t] - 1, static_cast<long long>(j) * 128, 128);
+        if (j >= it.lo_t[t] && j < it.hi_t[t]) edge |= j * 128 < it.full_lo[t] || j * 128 + 128 > it.full_hi[t];
     return edge;
 }
 
@@ -187,12 +201,14 @@ __device__ __forceinline__ int ext_page(const PagedFp8Params& c, int b, long lon
 // Columns [32 ch, 32 ch + 32) in which a V row of a masked tile that this row
 // may see holds a NaN code.
 template <int D>
-__device__ __noinline__ uint32_t ext_nan_columns(const ExtParams& p, int item, int t, int key_lo, int key_hi, int ch) {
+__device__ __noinline__ uint32_t ext_nan_columns(const ExtParams& p, int item, int t, int tok, int ch) {
     const ExtItem it = ext_item(p, item);
+    int key_lo, key_hi;
+    ext_keys(p.c, it.n, it.len, tok, &key_lo, &key_hi);
     uint32_t cols = 0;
     for (int j = it.lo_t[t]; j < it.hi_t[t]; ++j) {
         if (!ext_edge(it, j)) continue;
-        for (int k = j * 128 > key_lo ? j * 128 : key_lo; k <= key_hi && k < j * 128 + 128; ++k) {
+        for (int k = j * 128 > key_lo ? j * 128 : key_lo; k < key_hi && k < j * 128 + 128; ++k) {
             const long long row = (static_cast<long long>(ext_page(p.c, it.b, k)) << p.c.page_shift) + (k & ((1 << p.c.page_shift) - 1));
             const uint32_t* src = reinterpret_cast<const uint32_t*>(p.c.v + (row * p.c.Hkv + it.h) * D + ch * 32);
             for (int w = 0; w < 8; ++w) {
@@ -207,6 +223,18 @@ __device__ __noinline__ uint32_t ext_nan_columns(const ExtParams& p, int item, i
 
 __device__ __forceinline__ void sts_u2(uint32_t a, uint32_t x, uint32_t y) {
     asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
+
+// Two halves as hi + lo, both e4m3 (two codes in the low 16 bits).
+__device__ __forceinline__ void split_f16x2(uint32_t x, uint32_t& hi, uint32_t& lo) {
+    unsigned short h, l;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(x));
+    const uint32_t rest = e4m3x2_to_f16x2(h);
+    uint32_t d;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(rest));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(d));
+    hi = h;
+    lo = l;
 }
 
 // 16 codes to 16 halves, written as two 16-byte chunks.
@@ -270,7 +298,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
-        nan_round[0] = nan_round[1] = 0;
+        for (int e = 0; e < 4; ++e) nan_round[e] = 0;
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
@@ -310,9 +338,12 @@ __global__ void __launch_bounds__(384, 1)
             bool ok = true;
             const int boxes = 128 / p.box_rows;  // lane i < boxes loads keys [i*box_rows, (i+1)*box_rows) of a tile
             for (int round = 0; ok; ++round) {
-                int item = 0;
-                if (lane == 0) item = static_cast<int>(atomicAdd(p.counter, 1u));
-                item = __shfl_sync(0xffffffffu, item, 0);
+                // the first item by the CTA's index, further ones from the counter
+                int item = blockIdx.x;
+                if (round > 0) {
+                    if (lane == 0) item = static_cast<int>(gridDim.x + atomicAdd(p.counter, 1u));
+                    item = __shfl_sync(0xffffffffu, item, 0);
+                }
                 if (item >= p.n_items || item < 0) item = -1;
                 const int e = round & 1;
                 if (round >= 2) {
@@ -463,7 +494,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll 1
                     for (int half = 0; half < 2; ++half) {
                         const int r = half * 64 + (warp - 2) * 32 + lane;  // key row
-                        const long long key = static_cast<long long>(j) * 128 + r;
+                        const int key = j * 128 + r;
                         const bool seen = key >= it.k_lo && key < it.k_hi;
                         // 16 codes: chunk c of the row, exchanged by the TMA swizzle (128-byte rows: by row % 8, 64-byte
                         // rows: by row / 2 % 4); as f16, chunks 2c, 2c + 1 of 64-element (128-byte) columns of 128 rows
@@ -473,20 +504,29 @@ __global__ void __launch_bounds__(384, 1)
                             const int q = (2 * c) & 7;
                             sts_f16x16(row + ((q ^ (r & 7)) << 4), row + (((q + 1) ^ (r & 7)) << 4), v);
                         };
-                        if (!edge) {
+                        uint32_t hit = 0;  // bit 7 of every byte: a NaN code
+                        if (edge) {
+#pragma unroll 2
+                            for (int c = 0; c < D / 16; ++c) {
+                                const uint4 v = lds_u4(code_at(c));
+                                hit |= ((v.x & 0x7F7F7F7Fu) + 0x01010101u) | ((v.y & 0x7F7F7F7Fu) + 0x01010101u) |
+                                       ((v.z & 0x7F7F7F7Fu) + 0x01010101u) | ((v.w & 0x7F7F7F7Fu) + 0x01010101u);
+                            }
+                            hit &= 0x80808080u;
+                        }
+                        if (!edge || (seen && hit == 0)) {
 #pragma unroll
                             for (int c = 0; c < D / 16; ++c) put(c, lds_u4(code_at(c)));
                         } else {
 #pragma unroll 1
                             for (int c = 0; c < D / 16; ++c) {
-                                uint4 v = lds_u4(code_at(c));
-                                if (!seen) v = make_uint4(0u, 0u, 0u, 0u);
-                                nan |= has_nan4(v.x) || has_nan4(v.y) || has_nan4(v.z) || has_nan4(v.w);
+                                const uint4 v = seen ? lds_u4(code_at(c)) : make_uint4(0u, 0u, 0u, 0u);
                                 put(c, make_uint4(drop_nan4(v.x), drop_nan4(v.y), drop_nan4(v.z), drop_nan4(v.w)));
                             }
+                            nan |= seen;
                         }
                     }
-                    if (nan) nan_round[round & 1] = round + 1;
+                    if (nan) nan_round[round & 3] = round + 1;
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
@@ -507,239 +547,248 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t s_full = s_full0 + 8 * t, p_ready = p_ready0 + 8 * t, o_full = o_full0 + 8 * t;
         const int tok_of_row = row / p.c.g, head_of_row = row % p.c.g;
         uint32_t s_phase = 0, o_phase = 0, sc = 0;
-        bool ok = true;
-        for (int round = 0; ok; ++round) {
-            int item;
-            if (!next_item(round, &item)) break;
-            const ExtItem it = ext_item(p, item);
-            const int tok = it.tok[t] + tok_of_row;
-            const bool valid = tok_of_row < p.toks && tok < it.tok_end[t];
-            const long long q_row = (static_cast<long long>(it.sq.q0) + tok) * p.c.Hq + static_cast<long long>(it.h) * p.c.g + head_of_row;
-            float* lse = p.c.lse == nullptr ? nullptr
-                                            : p.c.lse + (static_cast<long long>(it.sq.q0) + tok) * p.c.lse_tok +
-                                                  (static_cast<long long>(it.h) * p.c.g + head_of_row) * p.c.lse_head;
-            const bool part = it.active > 1;  // a part writes its (o, lse) to the workspace
-            const long long ws_row = q_row * p.splits + it.split;
-            if (it.lo_t[t] >= it.hi_t[t]) {
-                // no key for any row of this tile
-                if (valid && part) {
-                    if (it.split < it.active) p.c.ws_lse[ws_row] = -CUDART_INF_F;
-                } else if (valid && it.split == 0) {
-                    uint4* dst = reinterpret_cast<uint4*>(p.c.o + q_row * D);
-#pragma unroll
-                    for (int v = 0; v < D / 8; ++v) dst[v] = make_uint4(0u, 0u, 0u, 0u);
-                    if (lse) *lse = -CUDART_INF_F;
-                }
-            } else {
-                // this thread's query row as two e4m3 terms
-                uint4 raw_q[D / 8];
-                float amax = 0.f;
-#pragma unroll
-                for (int v = 0; v < D / 8; ++v) {
-                    raw_q[v] = valid ? __ldg(reinterpret_cast<const uint4*>(p.c.q + q_row * D) + v) : make_uint4(0u, 0u, 0u, 0u);
-                }
-#pragma unroll
-                for (int v = 0; v < D / 8; ++v) {
-                    const uint32_t w[4] = {raw_q[v].x, raw_q[v].y, raw_q[v].z, raw_q[v].w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
-                }
-                // amax <= 448 * 2^e2, e2 within [-100, 120]
-                const uint32_t ab = __float_as_uint(amax);
-                int e2 = static_cast<int>(ab >> 23) - 127 - 8 + ((ab & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-                e2 = e2 < -100 ? -100 : (e2 > 120 ? 120 : e2);
-                const float down = pow2f(-e2);
-                const float c_row = p.c.scale_log2 * pow2f(e2);
-#pragma unroll
-                for (int v = 0; v < D / 8; ++v) {
-                    const uint32_t w[4] = {raw_q[v].x, raw_q[v].y, raw_q[v].z, raw_q[v].w};
-                    uint32_t hi[2], lo[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float f[4] = {__uint_as_float(w[2 * i] << 16), __uint_as_float(w[2 * i] & 0xFFFF0000u),
-                                      __uint_as_float(w[2 * i + 1] << 16), __uint_as_float(w[2 * i + 1] & 0xFFFF0000u)};
-                        // x - x: an infinity becomes NaN, as its scores would
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) f[e] = fmaf(f[e], down, f[e] - f[e]);
-                        hi[i] = pack_e4m3x4(f[0], f[1], f[2], f[3]);
-                        const float2 a = f16x2_to_float2(e4m3x2_to_f16x2(hi[i])), b = f16x2_to_float2(e4m3x2_hi_to_f16x2(hi[i]));
-                        lo[i] = pack_e4m3x4(f[0] - a.x, f[1] - a.y, f[2] - b.x, f[3] - b.y);
-                    }
-                    // 8 bytes of each term, in 128-byte rows swizzled by row % 8
-                    const uint32_t q_base = sQ + t * T::Q_BYTES + row * 128 + (v & 1) * 8;
-                    if constexpr (D == 128) {
-                        const uint32_t at = q_base + (((v >> 1) ^ (row & 7)) << 4);
-                        sts_u2(at, hi[0], hi[1]);
-                        sts_u2(at + 128 * 128, lo[0], lo[1]);
-                    } else {
-                        sts_u2(q_base + (((v >> 1) ^ (row & 7)) << 4), hi[0], hi[1]);
-                        sts_u2(q_base + (((4 + (v >> 1)) ^ (row & 7)) << 4), lo[0], lo[1]);
-                    }
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(q_full0 + 8 * t);
 
-                int key_lo, key_hi;  // keys of this row
-                row_col_bounds(it.band, tok, 0, &key_lo, &key_hi);
-                if (!valid) {
-                    key_lo = 1;
-                    key_hi = 0;
-                }
-                float my = -CUDART_INF_F, l = 0.f;
-                for (int j = it.lo; j < it.hi; ++j, ++sc) {
-                    const uint32_t ss = sc % T::SCALE_SLOTS;
-                    ok = warp_wait(sc_full0 + 8 * ss, (sc / T::SCALE_SLOTS) & 1u);
-                    if (!ok) break;
-                    if (j < it.lo_t[t] || j >= it.hi_t[t]) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(sc_empty0 + 8 * ss);
-                        continue;
+        // One turn: take an item (its row, and its query into shared memory), finish
+        // the item before (wait for its last product, write O), do the new item's
+        // key tiles.  So the tensor core starts on an item's first scores during the
+        // epilogue of the one before.
+        bool ok = true, pending = false;
+        // of the item in hand
+        int item = -1, tok = 0, split = 0, active = 0, round_of = 0;
+        bool valid = false, visited = false;  // a row of the problem; its tile has keys
+        long long q_row = 0;                  // row (token, query head) of q and o
+        float my = 0.f, l = 0.f;
+        for (int round = 0; ok; ++round) {
+            int n_item;
+            const bool have = next_item(round, &n_item);
+            int n_tok = 0, n_split = 0, n_active = 0, lo = 0, hi = 0, lo_u = 0, hi_u = 0, full_lo = 0, full_hi = 0, key_lo = 0, key_hi = 0;
+            bool n_valid = false;
+            long long n_row = 0;
+            float n_c = 0.f;
+            if (have) {
+                const ExtItem it = ext_item(p, n_item);
+                n_tok = it.tok[t] + tok_of_row;
+                n_valid = tok_of_row < p.toks && n_tok < it.tok_end[t];
+                n_split = it.split;
+                n_active = it.active;
+                lo = it.lo_t[t], hi = it.hi_t[t], lo_u = it.lo, hi_u = it.hi;
+                full_lo = it.full_lo[t], full_hi = it.full_hi[t];
+                if (n_valid) ext_keys(p.c, it.n, it.len, n_tok, &key_lo, &key_hi);
+                n_row = (static_cast<long long>(it.q0) + n_tok) * p.c.Hq + static_cast<long long>(it.h) * p.c.g + head_of_row;
+                if (lo < hi) {
+                    // this thread's query row as two e4m3 terms; the tile's products of the item before are done
+                    uint4 raw_q[D / 8];
+                    uint32_t ab = 0;  // the largest magnitude as bf16 bits: an infinity or a NaN is above every number
+#pragma unroll
+                    for (int v = 0; v < D / 8; ++v)
+                        raw_q[v] = n_valid ? __ldg(reinterpret_cast<const uint4*>(p.c.q + n_row * D) + v) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                    for (int v = 0; v < D / 8; ++v)
+                        ab = __vmaxu2(ab, __vmaxu2(__vmaxu2(raw_q[v].x & 0x7FFF7FFFu, raw_q[v].y & 0x7FFF7FFFu),
+                                                   __vmaxu2(raw_q[v].z & 0x7FFF7FFFu, raw_q[v].w & 0x7FFF7FFFu)));
+                    ab = (ab >> 16) > (ab & 0xFFFFu) ? ab >> 16 : ab & 0xFFFFu;
+                    // the row's largest magnitude <= 448 * 2^e2, e2 within [-100, 120]
+                    int e2 = static_cast<int>(ab >> 7) - 127 - 8 + ((ab & 0x7Fu) > 0x60u ? 1 : 0);
+                    e2 = e2 < -100 ? -100 : (e2 > 120 ? 120 : e2);
+                    const float down = ab >= 0x7F80u ? CUDART_NAN_F : pow2f(-e2);  // a row that is not finite becomes NaN
+                    n_c = p.c.scale_log2 * pow2f(e2);
+#pragma unroll
+                    for (int v = 0; v < D / 8; ++v) {
+                        const uint32_t w[4] = {raw_q[v].x, raw_q[v].y, raw_q[v].z, raw_q[v].w};
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            // f16 holds the scaled bf16 exactly (down to 2^-24), and so the difference
+                            split_f16x2(pack_f16x2(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xFFFF0000u) * down), hi[i], lo[i]);
+                        // 8 bytes of each term, in 128-byte rows swizzled by row % 8
+                        const uint32_t q_base = sQ + t * T::Q_BYTES + row * 128 + (v & 1) * 8;
+                        const uint32_t h0 = hi[0] | (hi[1] << 16), h1 = hi[2] | (hi[3] << 16);
+                        const uint32_t l0 = lo[0] | (lo[1] << 16), l1 = lo[2] | (lo[3] << 16);
+                        if constexpr (D == 128) {
+                            const uint32_t at = q_base + (((v >> 1) ^ (row & 7)) << 4);
+                            sts_u2(at, h0, h1);
+                            sts_u2(at + 128 * 128, l0, l1);
+                        } else {
+                            sts_u2(q_base + (((v >> 1) ^ (row & 7)) << 4), h0, h1);
+                            sts_u2(q_base + (((4 + (v >> 1)) ^ (row & 7)) << 4), l0, l1);
+                        }
                     }
-                    ok = warp_wait(s_full, s_phase & 1u);
-                    ++s_phase;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(q_full0 + 8 * t);
+                }
+            }
+            if (pending) {
+                const bool part = active > 1;  // a part writes its (o, lse) to the workspace
+                const long long ws_row = q_row * p.splits + split;
+                float* lse = nullptr;
+                if (p.c.lse != nullptr) lse = p.c.lse + q_row / p.c.Hq * p.c.lse_tok + q_row % p.c.Hq * p.c.lse_head;
+                if (!visited) {
+                    // no key for any row of this tile
+                    if (valid && part) {
+                        if (split < active) p.c.ws_lse[ws_row] = -CUDART_INF_F;
+                    } else if (valid && split == 0) {
+                        uint4* dst = reinterpret_cast<uint4*>(p.c.o + q_row * D);
+#pragma unroll
+                        for (int v = 0; v < D / 8; ++v) dst[v] = make_uint4(0u, 0u, 0u, 0u);
+                        if (lse) *lse = -CUDART_INF_F;
+                    }
+                } else {
+                    // O = acc / l, LSE = (my + log2 l - 7) ln 2
+                    ok = warp_wait(o_full, o_phase & 1u);
+                    ++o_phase;
                     if (!ok) break;
                     tc_fence_after_sync();
-                    uint32_t sr[4][32];
-#pragma unroll
-                    for (int q4 = 0; q4 < 4; ++q4) tmem_ld32(taddr_s + q4 * 32, sr[q4]);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int q4 = 0; q4 < 4; ++q4) reg_fence(sr[q4]);
-                    const int k0 = j * 128;
-                    if (!tile_is_full(it.band, it.tok[t], it.tok_end[t] - 1, k0, 128)) {
-                        const int lo_col = key_lo - k0, hi_col = key_hi - k0;
-#pragma unroll
-                        for (int c = 0; c < 128; ++c)
-                            if (c < lo_col || c > hi_col) sr[c >> 5][c & 31] = __float_as_uint(-CUDART_INF_F);
-                    }
-                    // the largest y, block by block
-                    const uint32_t sblk = sScale + ss * 128;
-                    float fk[8], mx = -CUDART_INF_F;
-#pragma unroll
-                    for (int blk = 0; blk < 8; ++blk) {
-                        const float2 s2 = lds_f2(sblk + blk * 16);
-                        // never 0, so that a masked score stays -inf
-                        fk[blk] = fmaxf(c_row * s2.x, 1e-37f);
-                        float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int c = blk * 16 + 4 * i;
-                            m0 = fmax3(m0, __uint_as_float(sr[c >> 5][c & 31]), __uint_as_float(sr[c >> 5][(c & 31) + 1]));
-                            m1 = fmax3(m1, __uint_as_float(sr[c >> 5][(c & 31) + 2]), __uint_as_float(sr[c >> 5][(c & 31) + 3]));
-                        }
-                        mx = fmaxf(mx, fmaf(fmaxf(m0, m1), fk[blk], s2.y));
-                    }
-                    float alpha = 1.f;
-                    bool resc = false;
-                    if (mx > my + kDp8Slack) {
-                        alpha = fast_exp2(my - mx);  // 0 when my is -inf
-                        resc = j > it.lo_t[t] && my != -CUDART_INF_F;
-                        my = mx;
-                        l *= alpha;
-                    }
-                    const float shift = kDp8Shift - (my == -CUDART_INF_F ? 0.f : my);
-                    uint32_t pk[2][32];
-#pragma unroll
-                    for (int blk = 0; blk < 8; ++blk) {
-                        const float4 s4 = lds128(sblk + blk * 16);  // ks, log2 vs, 1 / vs
-                        const uint64_t f2 = f2_pack(fk[blk], fk[blk]);
-                        const float sh = s4.y + shift;
-                        const uint64_t sh2 = f2_pack(sh, sh);
-                        uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int c = blk * 16 + 2 * i;
-                            const uint64_t y2 = f2_fma(f2_pack(__uint_as_float(sr[c >> 5][c & 31]), __uint_as_float(sr[c >> 5][(c & 31) + 1])), f2, sh2);
-                            float y0, y1;
-                            f2_unpack(y2, y0, y1);
-                            const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
-                            sum[i & 1] = f2_add(sum[i & 1], f2_pack(p0, p1));
-                            pk[c >> 6][(c >> 1) & 31] = pack_f16x2(p0, p1);
-                        }
-                        float a, b;
-                        f2_unpack(f2_add(sum[0], sum[1]), a, b);
-                        l = fmaf(a + b, s4.z, l);
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(sc_empty0 + 8 * ss);
-                    tmem_st32(taddr_s, pk[0]);
-                    tmem_st32(taddr_s + 32, pk[1]);
-                    if (__any_sync(0xffffffffu, resc)) {
-                        const float a = resc ? alpha : 1.f;
+                    const bool empty = my == -CUDART_INF_F && l == 0.f;
+                    const float inv_l = empty ? 0.f : 1.f / l;
+                    const bool nan = nan_round[round_of & 3] == round_of + 1;
+                    __nv_bfloat16* orow = p.c.o + q_row * D;
+                    float* wrow = part ? p.c.ws_o + ws_row * D : nullptr;
 #pragma unroll 1
-                        for (int ch = 0; ch < D / 32; ++ch) {
-                            uint32_t orr[32];
-                            tmem_ld32(taddr_o + ch * 32, orr);
-                            tmem_wait_ld();
-                            reg_fence(orr);
+                    for (int ch = 0; ch < D / 32; ++ch) {
+                        uint32_t orr[32];
+                        tmem_ld32(taddr_o + ch * 32, orr);
+                        tmem_wait_ld();
+                        reg_fence(orr);
+                        if (valid) {
+                            const uint32_t cols = nan ? ext_nan_columns<D>(p, item, t, tok, ch) : 0u;
+                            float f[32];
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * a);
-                            tmem_st32(taddr_o + ch * 32, orr);
+                            for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(orr[e]) * inv_l;
+                            if (cols != 0) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if ((cols >> e) & 1u) f[e] = CUDART_NAN_F;
+                            }
+                            if (part) {
+#pragma unroll
+                                for (int v = 0; v < 8; ++v)
+                                    reinterpret_cast<float4*>(wrow + ch * 32)[v] = make_float4(f[4 * v], f[4 * v + 1], f[4 * v + 2], f[4 * v + 3]);
+                            } else {
+#pragma unroll
+                                for (int v = 0; v < 4; ++v)
+                                    reinterpret_cast<uint4*>(orow + ch * 32)[v] =
+                                        make_uint4(pack_bf16x2(f[8 * v], f[8 * v + 1]), pack_bf16x2(f[8 * v + 2], f[8 * v + 3]),
+                                                   pack_bf16x2(f[8 * v + 4], f[8 * v + 5]), pack_bf16x2(f[8 * v + 6], f[8 * v + 7]));
+                            }
                         }
                     }
-                    tmem_wait_st();
-                    tc_fence_before_sync();
-                    mbar_arrive(p_ready);
-                }
-                if (!ok) break;
-                // O = acc / l, LSE = (my + log2 l - 7) ln 2
-                ok = warp_wait(o_full, o_phase & 1u);
-                ++o_phase;
-                if (!ok) break;
-                tc_fence_after_sync();
-                const bool empty = my == -CUDART_INF_F && l == 0.f;
-                const float inv_l = empty ? 0.f : 1.f / l;
-                const bool nan = nan_round[round & 1] == round + 1;
-                __nv_bfloat16* orow = p.c.o + q_row * D;
-                float* wrow = part ? p.c.ws_o + ws_row * D : nullptr;
-#pragma unroll 1
-                for (int ch = 0; ch < D / 32; ++ch) {
-                    uint32_t orr[32];
-                    tmem_ld32(taddr_o + ch * 32, orr);
-                    tmem_wait_ld();
-                    reg_fence(orr);
                     if (valid) {
-                        const uint32_t cols = nan ? ext_nan_columns<D>(p, item, t, key_lo, key_hi, ch) : 0u;
-                        float f[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(orr[e]) * inv_l;
-                        if (cols != 0) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if ((cols >> e) & 1u) f[e] = CUDART_NAN_F;
-                        }
-                        if (part) {
-#pragma unroll
-                            for (int v = 0; v < 8; ++v)
-                                reinterpret_cast<float4*>(wrow + ch * 32)[v] = make_float4(f[4 * v], f[4 * v + 1], f[4 * v + 2], f[4 * v + 3]);
-                        } else {
-#pragma unroll
-                            for (int v = 0; v < 4; ++v)
-                                reinterpret_cast<uint4*>(orow + ch * 32)[v] =
-                                    make_uint4(pack_bf16x2(f[8 * v], f[8 * v + 1]), pack_bf16x2(f[8 * v + 2], f[8 * v + 3]),
-                                               pack_bf16x2(f[8 * v + 4], f[8 * v + 5]), pack_bf16x2(f[8 * v + 6], f[8 * v + 7]));
-                        }
+                        const float lse2 = empty ? -CUDART_INF_F : my + fast_log2(l) - kDp8Shift;
+                        if (part) p.c.ws_lse[ws_row] = lse2;
+                        else if (lse) *lse = lse2 * 0.6931471805599453f;
                     }
+                    // the next item's first product overwrites O only once this tile's P is ready again,
+                    // which this warp signals after the reads above
+                    tc_fence_before_sync();
                 }
-                if (valid) {
-                    const float lse2 = empty ? -CUDART_INF_F : my + fast_log2(l) - kDp8Shift;
-                    if (part) p.c.ws_lse[ws_row] = lse2;
-                    else if (lse) *lse = lse2 * 0.6931471805599453f;
-                }
-                // the next item's first product may overwrite O once this tile's P is ready, which
-                // this warp signals only after the reads above
-                tc_fence_before_sync();
-                continue;
             }
-            // a tile without keys still takes part in the pair's scale ring
-            for (int j = it.lo; j < it.hi; ++j, ++sc) {
+            if (!have) break;
+            item = n_item, tok = n_tok, split = n_split, active = n_active, round_of = round;
+            valid = n_valid, visited = lo < hi, q_row = n_row, pending = true;
+            const float c_row = n_c;
+            my = -CUDART_INF_F;
+            l = 0.f;
+            for (int j = lo_u; j < hi_u; ++j, ++sc) {
                 const uint32_t ss = sc % T::SCALE_SLOTS;
                 ok = warp_wait(sc_full0 + 8 * ss, (sc / T::SCALE_SLOTS) & 1u);
                 if (!ok) break;
+                if (j < lo || j >= hi) {
+                    // a key tile of the other row tile still counts in the scale ring
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sc_empty0 + 8 * ss);
+                    continue;
+                }
+                ok = warp_wait(s_full, s_phase & 1u);
+                ++s_phase;
+                if (!ok) break;
+                tc_fence_after_sync();
+                uint32_t sr[4][32];
+#pragma unroll
+                for (int q4 = 0; q4 < 4; ++q4) tmem_ld32(taddr_s + q4 * 32, sr[q4]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int q4 = 0; q4 < 4; ++q4) reg_fence(sr[q4]);
+                const int k0 = j * 128;
+                if (k0 < full_lo || k0 + 128 > full_hi) {
+                    const int lo_col = key_lo - k0, hi_col = key_hi - k0;  // columns [lo_col, hi_col)
+#pragma unroll
+                    for (int blk = 0; blk < 8; ++blk) {
+                        // most blocks of a masked tile are whole for all of a warp's rows
+                        if (!__any_sync(0xffffffffu, blk * 16 < lo_col || blk * 16 + 16 > hi_col)) continue;
+#pragma unroll
+                        for (int c = blk * 16; c < blk * 16 + 16; ++c)
+                            if (c < lo_col || c >= hi_col) sr[c >> 5][c & 31] = __float_as_uint(-CUDART_INF_F);
+                    }
+                }
+                // the largest y, block by block
+                const uint32_t sblk = sScale + ss * 128;
+                float fk[8], mx = -CUDART_INF_F;
+#pragma unroll
+                for (int blk = 0; blk < 8; ++blk) {
+                    const float2 s2 = lds_f2(sblk + blk * 16);
+                    // never 0, so that a masked score stays -inf
+                    fk[blk] = fmaxf(c_row * s2.x, 1e-37f);
+                    float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = blk * 16 + 4 * i;
+                        m0 = fmax3(m0, __uint_as_float(sr[c >> 5][c & 31]), __uint_as_float(sr[c >> 5][(c & 31) + 1]));
+                        m1 = fmax3(m1, __uint_as_float(sr[c >> 5][(c & 31) + 2]), __uint_as_float(sr[c >> 5][(c & 31) + 3]));
+                    }
+                    mx = fmaxf(mx, fmaf(fmaxf(m0, m1), fk[blk], s2.y));
+                }
+                float alpha = 1.f;
+                bool resc = false;
+                if (mx > my + kDp8Slack) {
+                    alpha = fast_exp2(my - mx);  // 0 when my is -inf
+                    resc = j > lo && my != -CUDART_INF_F;
+                    my = mx;
+                    l *= alpha;
+                }
+                const float shift = kDp8Shift - (my == -CUDART_INF_F ? 0.f : my);
+                uint32_t pk[2][32];
+#pragma unroll
+                for (int blk = 0; blk < 8; ++blk) {
+                    const float4 s4 = lds128(sblk + blk * 16);  // ks, log2 vs, 1 / vs
+                    const uint64_t f2 = f2_pack(fk[blk], fk[blk]);
+                    const float sh = s4.y + shift;
+                    const uint64_t sh2 = f2_pack(sh, sh);
+                    uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int c = blk * 16 + 2 * i;
+                        const uint64_t y2 = f2_fma(f2_pack(__uint_as_float(sr[c >> 5][c & 31]), __uint_as_float(sr[c >> 5][(c & 31) + 1])), f2, sh2);
+                        float y0, y1;
+                        f2_unpack(y2, y0, y1);
+                        const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
+                        sum[i & 1] = f2_add(sum[i & 1], f2_pack(p0, p1));
+                        pk[c >> 6][(c >> 1) & 31] = pack_f16x2(p0, p1);
+                    }
+                    float a, b;
+                    f2_unpack(f2_add(sum[0], sum[1]), a, b);
+                    l = fmaf(a + b, s4.z, l);
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(sc_empty0 + 8 * ss);
+                tmem_st32(taddr_s, pk[0]);
+                tmem_st32(taddr_s + 32, pk[1]);
+                if (__any_sync(0xffffffffu, resc)) {
+                    const float a = resc ? alpha : 1.f;
+#pragma unroll 1
+                    for (int ch = 0; ch < D / 32; ++ch) {
+                        uint32_t orr[32];
+                        tmem_ld32(taddr_o + ch * 32, orr);
+                        tmem_wait_ld();
+                        reg_fence(orr);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * a);
+                        tmem_st32(taddr_o + ch * 32, orr);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before_sync();
+                mbar_arrive(p_ready);
             }
         }
     }
@@ -758,19 +807,22 @@ __global__ void __launch_bounds__(384, 1)
     }
 }
 
-// One row (token, query head) per warp: merge its parts.
+// 16 rows of a pair of row tiles per CTA, two to a warp: merge their parts.
 template <int D>
-__global__ void __launch_bounds__(128) merge_ext_kernel(const __grid_constant__ ExtParams p) {
+__global__ void __launch_bounds__(256) merge_ext_kernel(const __grid_constant__ ExtParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const long long item = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const long long per_seq = static_cast<long long>(p.c.max_q) * p.c.Hq;
-    const int b = static_cast<int>(item / per_seq), w = static_cast<int>(item % per_seq);
-    if (b >= p.c.B) return;
-    const int i = w / p.c.Hq, hq = w % p.c.Hq;
-    const SeqSpan sq = seq_span(p.c, b);
-    if (i >= (sq.n < p.c.max_q ? sq.n : p.c.max_q)) return;
-    const ExtItem it = ext_pair(p, b, hq / p.c.g, i / p.toks / 2, 0);
-    if (it.active > 1) merge_row<D>(p.c, sq, i, hq, it.active, p.splits);
+    const int x = blockIdx.x >> 4;
+    const int bh = x / p.n_pairs, pair = x % p.n_pairs;
+    const int h = bh % p.c.Hkv;
+    const ExtItem it = ext_pair(p, bh / p.c.Hkv, h, pair, 0);
+    if (it.active <= 1) return;
+    const int rows = (it.tok_end[1] - it.tok[0]) * p.c.g;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int r = (blockIdx.x & 15) * 16 + e * 8 + (threadIdx.x >> 5);
+        if (r < rows)
+            merge_row<D>(p.c, static_cast<long long>(it.q0) + it.tok[0] + r / p.c.g, h * p.c.g + r % p.c.g, it.active, p.splits);
+    }
 }
 
 }  // namespace fattn

@@ -56,11 +56,23 @@
 
 namespace fattn {
 
+#ifndef DPT
+#define DPT 1280
+#endif
+#ifndef DPM
+#define DPM 16
+#endif
 constexpr int DP8_WARPS = 4;
 constexpr int DP8_BLOCK = 16;       // keys per warp step
-constexpr int DP8_MIN_BLOCKS = 16;  // key blocks of the smallest split: 256 keys
+constexpr int DP8_MIN_BLOCKS = DPM;  // key blocks of the smallest split: 256 keys
 // CTAs the automatic split aims at: 2.9 waves of 3 CTAs on 148 SMs.
-constexpr int kDp8TargetCtas = 1280;
+#ifndef DPT
+#define DPT 1280
+#endif
+#ifndef DPM
+#define DPM 16
+#endif
+constexpr int kDp8TargetCtas = DPT;
 constexpr float kDp8Shift = 7.f;    // p' = 2^(y - my + 7)
 constexpr float kDp8Slack = 8.f;
 constexpr float kMinValueScale = 7.888609052210118e-31f;  // 2^-100: smaller V scales count as this
@@ -628,40 +640,36 @@ __global__ void __launch_bounds__(32 * DP8_WARPS) decode_paged_fp8_kernel(const 
     }
 }
 
-// One warp: the row of token i and query head hq of a sequence from its
-// `active` partial (o, lse) pairs, `stride` of them to a row in the workspace.
+// One warp: the row of packed token tok and query head hq from its `active` partial (o, lse) pairs, `stride` of them to a row in the workspace.
 template <int D>
-__device__ __forceinline__ void merge_row(const PagedFp8Params& p, const SeqSpan& sq, int i, int hq, int active, int stride) {
+__device__ __forceinline__ void merge_row(const PagedFp8Params& p, long long tok, int hq, int active, int stride) {
     constexpr int EPL = D / 32;  // elements per lane
     const int lane = threadIdx.x & 31;
-    const long long r = (static_cast<long long>(sq.q0) + i) * p.Hq + hq;
+    const long long r = tok * p.Hq + hq;
     const float* ls = p.ws_lse + r * stride;
-    float M = -CUDART_INF_F;
-    bool nan = false;
-    for (int s = lane; s < active; s += 32) {
-        const float x = ls[s];
-        nan |= x != x;
-        M = fmaxf(M, x);
-    }
+    // lane s holds the lse of parts s and s + 32 (at most 64 parts)
+    const float x0 = lane < active ? ls[lane] : -CUDART_INF_F, x1 = lane + 32 < active ? ls[lane + 32] : -CUDART_INF_F;
+    const bool nan = __any_sync(0xffffffffu, x0 != x0 || x1 != x1);
+    float M = fmaxf(x0, x1);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    nan = __any_sync(0xffffffffu, nan);
     const float safe = M == -CUDART_INF_F ? 0.f : M;
+    const float w0 = fast_exp2(x0 - safe), w1 = fast_exp2(x1 - safe);
     float W = 0.f, f[EPL];
 #pragma unroll
     for (int e = 0; e < EPL; ++e) f[e] = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < active; ++s) {
-        const float x = ls[s];
-        if (x == -CUDART_INF_F) continue;  // no key of this row: its o may not have been written
-        const float wt = fast_exp2(x - safe);
+    const float* src = p.ws_o + r * stride * D + lane * EPL;
+#pragma unroll 8
+    for (int s = 0; s < active; ++s, src += D) {
+        const float wt = __shfl_sync(0xffffffffu, s < 32 ? w0 : w1, s & 31);
+        const bool some = __shfl_sync(0xffffffffu, s < 32 ? x0 : x1, s & 31) != -CUDART_INF_F;
         W += wt;
-        const float* src = p.ws_o + (r * stride + s) * D + lane * EPL;
+        // a part without a key of this row may not have written its o
         if constexpr (EPL == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(src);
+            const float4 v = some ? *reinterpret_cast<const float4*>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
             f[0] = fmaf(wt, v.x, f[0]), f[1] = fmaf(wt, v.y, f[1]), f[2] = fmaf(wt, v.z, f[2]), f[3] = fmaf(wt, v.w, f[3]);
         } else {
-            const float2 v = *reinterpret_cast<const float2*>(src);
+            const float2 v = some ? *reinterpret_cast<const float2*>(src) : make_float2(0.f, 0.f);
             f[0] = fmaf(wt, v.x, f[0]), f[1] = fmaf(wt, v.y, f[1]);
         }
     }
@@ -671,7 +679,7 @@ __device__ __forceinline__ void merge_row(const PagedFp8Params& p, const SeqSpan
     dst[0] = pack_bf16x2(f[0] * inv, f[1] * inv);
     if constexpr (EPL == 4) dst[1] = pack_bf16x2(f[2] * inv, f[3] * inv);
     if (lane == 0 && p.lse != nullptr)
-        p.lse[(static_cast<long long>(sq.q0) + i) * p.lse_tok + static_cast<long long>(hq) * p.lse_head] =
+        p.lse[tok * p.lse_tok + static_cast<long long>(hq) * p.lse_head] =
             empty ? -CUDART_INF_F : (M + fast_log2(W)) * 0.6931471805599453f;
 }
 
@@ -692,7 +700,7 @@ __global__ void __launch_bounds__(128) merge_paged_fp8_kernel(const PagedFp8Para
     const int row0 = row / tile_rows * tile_rows;
     const int rows = n_tok * p.g - row0 < tile_rows ? n_tok * p.g - row0 : tile_rows;
     const SplitSpan sp = split_span(p, sq, row0 / p.g, (row0 + rows - 1) / p.g, 0);
-    if (sp.active > 1) merge_row<D>(p, sq, i, hq, sp.active, p.S);  // else written by the split kernel
+    if (sp.active > 1) merge_row<D>(p, static_cast<long long>(sq.q0) + i, hq, sp.active, p.S);  // else written by the split kernel
 }
 
 }  // namespace fattn

@@ -49,12 +49,12 @@ int launch_dp8_kernel(const PagedFp8Params& p, unsigned grid, cudaStream_t s) {
     return cudaGetLastError() == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
 
-// A merge kernel of one warp per row, set up while the kernel before it runs.
+// A merge kernel, set up while the kernel before it runs.
 template <typename... Args>
-int launch_merge(void (*kernel)(Args...), long long rows, cudaStream_t s, Args... args) {
+int launch_merge(void (*kernel)(Args...), long long grid, int threads, cudaStream_t s, Args... args) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4));
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(threads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -120,14 +120,14 @@ int launch_dp8(PagedFp8Params p, int d, int num_splits, void* workspace, size_t 
         else st = masked ? launch_dp8_kernel<64, 2, true>(p, grid, s) : launch_dp8_kernel<64, 2, false>(p, grid, s);
     }
     if (st != FATTN_OK || p.S == 1) return st;
-    const long long all = static_cast<long long>(p.B) * p.max_q * p.Hq;
-    return d == 128 ? launch_merge(merge_paged_fp8_kernel<128>, all, s, p, tile_rows)
-                    : launch_merge(merge_paged_fp8_kernel<64>, all, s, p, tile_rows);
+    const long long merge_grid = (static_cast<long long>(p.B) * p.max_q * p.Hq + 3) / 4;  // a warp per row
+    return d == 128 ? launch_merge(merge_paged_fp8_kernel<128>, merge_grid, 128, s, p, tile_rows)
+                    : launch_merge(merge_paged_fp8_kernel<64>, merge_grid, 128, s, p, tile_rows);
 }
 
 // Rows (new tokens x group heads) of a sequence from which its tiles go to the
 // tensor-core kernel.
-constexpr long long kExtMinRows = 65;
+constexpr long long kExtMinRows = 49;
 // Its TMA coordinates are 32-bit rows of the pool.
 constexpr long long kExtMaxPoolRows = 0x7fffff00LL;
 
@@ -139,17 +139,24 @@ long long ext_pairs(long long max_q, int g) {
     return ((max_q + toks - 1) / toks + 1) / 2;
 }
 
-#ifndef EXT_TARGET
-#define EXT_TARGET 444
-#endif
-// Parts of an item's key tiles: enough that the items fill 148 SMs three times
-// over, at least EXT_MIN_TILES tiles to a part.
-int ext_splits(long long items, int Lk) {
-    long long S = (EXT_TARGET + items - 1) / items;
-    const long long most = (static_cast<long long>(Lk) + 128 * EXT_MIN_TILES - 1) / (128 * EXT_MIN_TILES);
-    S = S > 32 ? 32 : S;
-    S = S > most ? most : S;
-    return static_cast<int>(S < 1 ? 1 : S);
+// Parts of an item's key tiles: the count with the shortest time by a model of
+// the kernel, whole rounds of one item per SM.  Measured on B200: 2.1 us a key
+// tile, 8 us more an item, 5 us for the merge and 1.6 TB/s for the parts' (o, lse).  16 items over 64 tiles: 47 us in 8 parts, 62 in 10, 64 in 16; 128 items
+// over 16 tiles: 52 us whole, 57 in 2 parts, 64 in 3.
+int ext_splits(long long items, long long tiles, long long rows, int d) {
+    const double sms = 148.0;
+    int best = 1;
+    double least = 0.0;
+    for (int S = 1; S <= 32 && (S == 1 || static_cast<long long>(S) * EXT_MIN_TILES <= tiles); ++S) {
+        const double rounds = std::ceil(static_cast<double>(items) * S / sms);
+        double us = rounds * (std::ceil(static_cast<double>(tiles) / S) * 2.1 + 8.0);
+        if (S > 1) us += 5.0 + static_cast<double>(rows) * S * (d + 1) * 8 / 1.6e6;
+        if (S == 1 || us < least) {
+            least = us;
+            best = S;
+        }
+    }
+    return best;
 }
 
 // The item counter, then the parts' (o, lse).
@@ -187,9 +194,17 @@ int launch_ext(const PagedFp8Params& c, int d, long long pool_rows, void* worksp
     p.toks = 128 / c.g;
     p.n_pairs = static_cast<int>(ext_pairs(c.max_q, c.g));
     const long long items = static_cast<long long>(c.B) * c.Hkv * p.n_pairs;
-    p.splits = ext_splits(items, c.max_pages << c.page_shift);
-    const long long n_items = items * p.splits, rows = static_cast<long long>(c.total_q) * c.Hq;
-    if (n_items > 0x7fff0000LL || static_cast<long long>(c.B) * c.max_q * c.Hq > 0x7fffffffLL) return FATTN_ERR_UNSUPPORTED;
+    const long long rows = static_cast<long long>(c.total_q) * c.Hq;
+    const long long all_tiles = ((static_cast<long long>(c.max_pages) << c.page_shift) + 127) / 128;
+    p.splits = ext_splits(items, all_tiles, rows, d);  // what the workspace is sized for
+    if (c.window_left >= 0 && (c.causal || c.window_right >= 0)) {
+        // a pair of row tiles sees the window and its own tokens
+        const long long seen = (static_cast<long long>(c.window_left) + (c.causal ? 0 : c.window_right) + 2LL * p.toks + 255) / 128;
+        const int S = ext_splits(items, seen < all_tiles ? seen : all_tiles, rows, d);
+        p.splits = S < p.splits ? S : p.splits;
+    }
+    const long long n_items = items * p.splits;
+    if (n_items > 0x7fff0000LL || items > 0x07ffffffLL || static_cast<long long>(c.B) * c.max_q * c.Hq > 0x7fffffffLL) return FATTN_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < ext_workspace(rows, p.splits, d)) return FATTN_ERR_WORKSPACE;
     if (!aligned16(workspace)) return FATTN_ERR_MISALIGNED;
     p.counter = static_cast<unsigned int*>(workspace);
@@ -216,8 +231,7 @@ int launch_ext(const PagedFp8Params& c, int d, long long pool_rows, void* worksp
     else attn_paged_fp8_kernel<64><<<grid, ExtTraits<64>::THREADS, ExtTraits<64>::SMEM_BYTES, s>>>(mk, mv, p);
     if (cudaGetLastError() != cudaSuccess) return FATTN_ERR_CUDA;
     if (p.splits == 1) return FATTN_OK;
-    const long long all = static_cast<long long>(c.B) * c.max_q * c.Hq;
-    return d == 128 ? launch_merge(merge_ext_kernel<128>, all, s, p) : launch_merge(merge_ext_kernel<64>, all, s, p);
+    return d == 128 ? launch_merge(merge_ext_kernel<128>, 16 * items, 256, s, p) : launch_merge(merge_ext_kernel<64>, 16 * items, 256, s, p);
 }
 
 template <int D, int WARPS>
@@ -352,7 +366,7 @@ size_t attn_fwd_paged_fp8_workspace_bytes(int B, int total_q, int max_seqlen_q, 
     const int g = Hq / Hkv;
     const long long rows = max_q * g, all = static_cast<long long>(total_q) * Hq;
     if (g <= 128 && ext_path(max_q, g))
-        return ext_workspace(all, ext_splits(static_cast<long long>(B) * Hkv * ext_pairs(max_q, g), Lk), d);
+        return ext_workspace(all, ext_splits(static_cast<long long>(B) * Hkv * ext_pairs(max_q, g), (static_cast<long long>(Lk) + 127) / 128, all, d), d);
     const int t = dp8_tile_rows(rows);
     const int S = dp8_auto_splits(static_cast<long long>(B) * Hkv * ((rows + t - 1) / t), Lk);
     return dp8_workspace(all, S, d);
