@@ -123,7 +123,7 @@ __device__ __forceinline__ ExtItem ext_pair(const ExtParams& p, int b, int h, in
     const SeqSpan sq = seq_span(p.c, b);
     it.q0 = sq.q0;
     it.n = sq.n;
-    it.len = static_cast<int>(sq.len);
+    it.len = sq.len;
     // rows behind max_seqlen_q are not computed, but they count for the alignment
     const int n_tok = it.n < p.c.max_q ? it.n : p.c.max_q;
     it.lo = it.k_lo = 0x7fffffff;

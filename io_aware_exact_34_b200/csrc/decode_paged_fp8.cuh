@@ -56,23 +56,12 @@
 
 namespace fattn {
 
-#ifndef DPT
-#define DPT 1280
-#endif
-#ifndef DPM
-#define DPM 16
-#endif
 constexpr int DP8_WARPS = 4;
 constexpr int DP8_BLOCK = 16;       // keys per warp step
-constexpr int DP8_MIN_BLOCKS = DPM;  // key blocks of the smallest split: 256 keys
+constexpr int DP8_MIN_BLOCKS = 16;   // key blocks of the smallest split: 256 keys
+constexpr int DP8_ROUND_BLOCKS = 4;  // a split's blocks: as many for each warp
 // CTAs the automatic split aims at: 2.9 waves of 3 CTAs on 148 SMs.
-#ifndef DPT
-#define DPT 1280
-#endif
-#ifndef DPM
-#define DPM 16
-#endif
-constexpr int kDp8TargetCtas = DPT;
+constexpr int kDp8TargetCtas = 1280;
 constexpr float kDp8Shift = 7.f;    // p' = 2^(y - my + 7)
 constexpr float kDp8Slack = 8.f;
 constexpr float kMinValueScale = 7.888609052210118e-31f;  // 2^-100: smaller V scales count as this
@@ -95,10 +84,10 @@ struct PagedFp8Params {
     float scale_log2;
 };
 
-// One sequence: first token, tokens, keys.
+// One sequence: first token, tokens, keys.  Lengths stay below 2^31, so all of
+// this is 32-bit arithmetic (a 64-bit division costs as much as a key block).
 struct SeqSpan {
-    int q0, n;
-    long long len;
+    int q0, n, len;
 };
 
 __device__ __forceinline__ SeqSpan seq_span(const PagedFp8Params& p, int b) {
@@ -111,33 +100,34 @@ __device__ __forceinline__ SeqSpan seq_span(const PagedFp8Params& p, int b) {
         s.q0 = b;
         s.n = 1;
     }
-    const long long cap = static_cast<long long>(p.max_pages) << p.page_shift;
-    const long long len = __ldg(p.seqlens_k + b);
+    const int cap = p.max_pages << p.page_shift;
+    const int len = __ldg(p.seqlens_k + b);
     s.len = len < 0 ? 0 : (len > cap ? cap : len);
     return s;
 }
 
-// Keys [lo, hi) that the token i of the sequence may see.
-__device__ __forceinline__ void key_range(const PagedFp8Params& p, const SeqSpan& s, long long i, long long* lo, long long* hi) {
-    const long long pos = i + s.len - s.n;
-    long long h = s.len, l = 0;
-    if (p.causal && pos + 1 < h) h = pos + 1;
-    if (!p.causal && p.window_right >= 0 && pos + p.window_right + 1 < h) h = pos + p.window_right + 1;
-    if (p.window_left >= 0 && pos - p.window_left > 0) l = pos - p.window_left;
+// Keys [lo, hi) that the token i of the sequence may see; both rise with i.
+__device__ __forceinline__ void key_range(const PagedFp8Params& p, const SeqSpan& s, int i, int* lo, int* hi) {
+    const int pos = i + (s.len - s.n);  // at most len - 1
+    const int room = s.len - 1 - pos;   // keys behind the token's own
+    const int right = p.causal ? 0 : p.window_right;
+    int h = s.len, l = 0;
+    if (right >= 0 && right < room) h = pos + right + 1;
+    if (p.window_left >= 0 && pos > p.window_left) l = pos - p.window_left;
     *lo = l;
     *hi = h > l ? h : l;
 }
 
 // The key blocks of the rows' union and this split's share.
 struct SplitSpan {
-    long long k_lo, k_hi;   // union of the rows' keys
-    long long first, last;  // blocks of this split
-    int active;             // splits that hold blocks
+    int k_lo, k_hi;   // union of the rows' keys
+    int first, last;  // blocks of this split
+    int active;       // splits that hold blocks
 };
 
-__device__ __forceinline__ SplitSpan split_span(const PagedFp8Params& p, const SeqSpan& s, long long tok_lo, long long tok_hi, int split) {
+__device__ __forceinline__ SplitSpan split_span(const PagedFp8Params& p, const SeqSpan& s, int tok_lo, int tok_hi, int split) {
     SplitSpan r;
-    long long lo0, hi0, lo1, hi1;
+    int lo0, hi0, lo1, hi1;
     key_range(p, s, tok_lo, &lo0, &hi0);
     key_range(p, s, tok_hi, &lo1, &hi1);
     r.k_lo = lo0;
@@ -145,11 +135,13 @@ __device__ __forceinline__ SplitSpan split_span(const PagedFp8Params& p, const S
     r.first = r.last = 0;
     r.active = 0;
     if (r.k_hi <= r.k_lo) return r;
-    const long long b0 = r.k_lo / DP8_BLOCK, b1 = (r.k_hi + DP8_BLOCK - 1) / DP8_BLOCK;
-    long long per = (b1 - b0 + p.S - 1) / p.S;
-    per = (per + DP8_MIN_BLOCKS - 1) / DP8_MIN_BLOCKS * DP8_MIN_BLOCKS;
-    r.active = static_cast<int>((b1 - b0 + per - 1) / per);
-    r.first = b0 + split * per;
+    const int b0 = r.k_lo / DP8_BLOCK, b1 = (r.k_hi - 1) / DP8_BLOCK + 1;
+    int per = (b1 - b0 + p.S - 1) / p.S;
+    per = (per + DP8_ROUND_BLOCKS - 1) / DP8_ROUND_BLOCKS * DP8_ROUND_BLOCKS;
+    per = per < DP8_MIN_BLOCKS ? DP8_MIN_BLOCKS : per;
+    r.active = (b1 - b0 + per - 1) / per;
+    const long long first = b0 + static_cast<long long>(split) * per;
+    r.first = first < b1 ? static_cast<int>(first) : b1;
     r.last = r.first + per < b1 ? r.first + per : b1;
     return r;
 }
@@ -280,28 +272,28 @@ __global__ void __launch_bounds__(32 * DP8_WARPS) decode_paged_fp8_kernel(const 
 
     // element offset of a row in q and o, and its place in lse
     auto row_q = [&](int r) -> long long {
-        const int i = (row0 + r) / p.g, j = (row0 + r) % p.g;
+        const int i = (row0 + r) / p.g, j = (row0 + r) - i * p.g;
         return ((static_cast<long long>(sq.q0) + i) * p.Hq + static_cast<long long>(h) * p.g + j) * D;
     };
     auto row_lse = [&](int r) -> long long {
-        const int i = (row0 + r) / p.g, j = (row0 + r) % p.g;
+        const int i = (row0 + r) / p.g, j = (row0 + r) - i * p.g;
         return (static_cast<long long>(sq.q0) + i) * p.lse_tok + (static_cast<long long>(h) * p.g + j) * p.lse_head;
     };
 
     const uint32_t ring = smem_addr(dp8_smem) + warp * T::WARP_BYTES;
     const uint32_t sring = smem_addr(dp8_smem) + T::RING_BYTES + warp * T::STAGES * 8;
-    const long long nblk = sp.last - sp.first;
-    const int nsteps = sp.active == 0 ? 0 : static_cast<int>((nblk - warp + DP8_WARPS - 1) / DP8_WARPS);
+    const int nblk = sp.last - sp.first;
+    const int nsteps = nblk <= warp ? 0 : (nblk - warp + DP8_WARPS - 1) / DP8_WARPS;
     const int shift = p.page_shift;
     const long long head_row = static_cast<long long>(p.Hkv) * D;  // bytes between a head's rows
     const int* table = p.block_table + static_cast<long long>(b) * p.max_pages;
 
     // keys of a step relative to the union's first; the union holds k_len keys
-    const int k_len = static_cast<int>(sp.k_hi - sp.k_lo);
-    const int rel_first = static_cast<int>((sp.first + warp) * DP8_BLOCK - sp.k_lo);
+    const int k_len = sp.k_hi - sp.k_lo;
+    const int rel_first = (sp.first + warp) * DP8_BLOCK - sp.k_lo;
     auto rel_of = [&](int i) { return rel_first + i * (DP8_WARPS * DP8_BLOCK); };
     const int page_mask = (1 << shift) - 1;
-    const int key_first = static_cast<int>((sp.first + warp) * DP8_BLOCK);  // absolute: tables hold at most 2^31 keys
+    const int key_first = (sp.first + warp) * DP8_BLOCK;  // absolute
     const int cr = lane / T::CPR, cc = lane % T::CPR;  // row and chunk of this lane in a copy
     const long long lane_off = static_cast<long long>(h) * D + cr * head_row + cc * 16;
     const uint8_t *k_lane = p.k + lane_off, *v_lane = p.v + lane_off;
@@ -390,19 +382,19 @@ __global__ void __launch_bounds__(32 * DP8_WARPS) decode_paged_fp8_kernel(const 
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int rr = nt * 8 + 2 * c4 + e;
-                long long lo = sp.k_lo, hi = sp.k_lo;  // rows of the padding see nothing
+                int lo = sp.k_lo, hi = sp.k_lo;  // rows of the padding see nothing
                 if (rr < rows) key_range(p, sq, (row0 + rr) / p.g, &lo, &hi);
-                klo[nt][e] = static_cast<int>(lo - sp.k_lo);
-                khi[nt][e] = static_cast<int>(hi - sp.k_lo);
+                klo[nt][e] = lo - sp.k_lo;
+                khi[nt][e] = hi - sp.k_lo;
             }
         }
     }
     if constexpr (kMasked) {
-        long long lo0, hi0, lo1, hi1;
+        int lo0, hi0, lo1, hi1;
         key_range(p, sq, row0 / p.g, &lo0, &hi0);
         key_range(p, sq, (row0 + rows - 1) / p.g, &lo1, &hi1);
-        full_lo = static_cast<int>(lo1 - sp.k_lo);
-        full_hi = static_cast<int>(hi0 - sp.k_lo);
+        full_lo = lo1 - sp.k_lo;
+        full_hi = hi0 - sp.k_lo;
     }
 
     float my[NT][2], l[NT][2], acc[NT][MT][4];
@@ -589,16 +581,15 @@ __global__ void __launch_bounds__(32 * DP8_WARPS) decode_paged_fp8_kernel(const 
             t += __shfl_xor_sync(0xffffffffu, t, 8);
             t += __shfl_xor_sync(0xffffffffu, t, 16);
             const int r = nt * 8 + 2 * c4 + e;
+            if (r >= rows) continue;
             if (r8 == 0) {
                 sm_m[warp * ROWS + r] = my[nt][e];
                 sm_l[warp * ROWS + r] = t;
             }
-            float* dst = sm_acc + (warp * ROWS + r) * LD + r8 * T::VB;
+            float4* dst = reinterpret_cast<float4*>(sm_acc + (warp * ROWS + r) * LD + r8 * T::VB);
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                dst[2 * i] = acc[nt][i][e];
-                dst[2 * i + 1] = acc[nt][i][e + 2];
-            }
+            for (int i = 0; i < MT / 2; ++i)
+                dst[i] = make_float4(acc[nt][2 * i][e], acc[nt][2 * i][e + 2], acc[nt][2 * i + 1][e], acc[nt][2 * i + 1][e + 2]);
         }
     __syncthreads();
     // Eight elements of a row per thread.
@@ -687,12 +678,11 @@ __device__ __forceinline__ void merge_row(const PagedFp8Params& p, long long tok
 template <int D>
 __global__ void __launch_bounds__(128) merge_paged_fp8_kernel(const PagedFp8Params p, int tile_rows) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const long long item = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const long long per_seq = static_cast<long long>(p.max_q) * p.Hq;
-    const int b = static_cast<int>(item / per_seq), w = static_cast<int>(item % per_seq);
+    const unsigned item = blockIdx.x * 4 + (threadIdx.x >> 5), per_seq = p.max_q * p.Hq;
+    const int b = item / per_seq, w = item - b * per_seq;
     if (b >= p.B) return;
     const SeqSpan sq = seq_span(p, b);
-    const int i = w / p.Hq, hq = w % p.Hq;
+    const int i = w / p.Hq, hq = w - i * p.Hq;
     const int n_tok = sq.n < p.max_q ? sq.n : p.max_q;
     if (i >= n_tok) return;
     // the tile of this row, whose union of keys was split
