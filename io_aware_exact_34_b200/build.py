@@ -1,4 +1,5 @@
-"""Build ``libfattn.so`` in-tree with nvcc for sm_100a.
+"""Build ``libfattn.so`` in-tree with nvcc for sm_100a, and ``_fattn_calls.so``,
+the native part of its Python binding, with g++ against the installed torch.
 
     python -m io_aware_exact_34_b200.build [--verbose]
 
@@ -8,18 +9,22 @@ GPU (every entry point then reports FATTN_ERR_NO_DEVICE).
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "fattn_api.cu")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfattn.so")
-DEPS = [os.path.join(PKG, "csrc", f) for f in os.listdir(os.path.join(PKG, "csrc"))] + [
+DEPS = [os.path.join(PKG, "csrc", f) for f in os.listdir(os.path.join(PKG, "csrc")) if f.endswith((".cu", ".cuh"))] + [
     os.path.join(INCLUDE, "fattn.h")]
+CALLS_SRC = os.path.join(PKG, "csrc", "binding.cpp")
+CALLS = os.path.join(PKG, "_fattn_calls.so")
 
 
 def _nvcc() -> str:
@@ -36,7 +41,27 @@ def needs_build() -> bool:
     return any(os.path.getmtime(p) > t for p in DEPS)
 
 
+def build_calls(force: bool = False) -> str:
+    """The binding's native calls (no CUDA code: any host compiler)."""
+    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= os.path.getmtime(CALLS_SRC):
+        return CALLS
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared"]
+    for d in (os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+              sysconfig.get_paths()["include"], os.path.join(cuda, "include")):
+        cmd += ["-isystem", d]
+    cmd += [CALLS_SRC, "-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-o", tmp]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + res.stdout + res.stderr)
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_calls(force)
     if not force and not needs_build():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
