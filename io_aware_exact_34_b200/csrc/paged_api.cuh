@@ -20,33 +20,65 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
-// Query-row tiles of one sequence and kv head in the split kernel: 8 rows to a
-// CTA while they hold a whole group, else 16.
-int dp8_tile_rows(long long rows) { return rows <= 8 ? 8 : 16; }
+// Query rows of one sequence and kv head that a CTA of the split kernel takes, 8
+// or 16.  Two tiles of 8 read the keys twice (the second time from L2) but need
+// half the registers: with several tokens a sequence that pays up to 32 rows (16
+// sequences of up to 2048 keys, 20 rows: 24.8 us in tiles of 8, 26.9 in tiles of
+// 16; 48 rows: 39.4 and 36.9).
+int dp8_tile_rows(long long rows, bool masked) { return rows <= (masked ? 32 : 8) ? 8 : 16; }
 
-int dp8_auto_splits(long long tiles, int Lk) {
-    // About kDp8TargetCtas CTAs: several waves, so that uneven sequences even
-    // out, without many short splits; a split holds at least 256 keys (the
-    // kernel keeps to that by each sequence's own length).  Measured at 3 to
-    // 16 splits of 256 tiles: 32 x 32768 keys 344-355 us at 5-16 splits, 361-370
-    // at 3-4, 369-379 at 24-32; 32 sequences of 1-8192 keys 62-63 us at 4-6
-    // splits, 66 at 3, 70-107 at 12-32; one sequence of 4097 keys (8 tiles):
-    // 10.2 us at 16 splits, 11.7 at 8 and at 32.
-    long long S = (kDp8TargetCtas + tiles / 2) / tiles;
+// CTAs of the split kernel that an SM holds (shared memory and registers).
+int dp8_resident(int d, int tile_rows, bool masked) {
+    if (d == 128) return masked && tile_rows > 8 ? 2 : 3;
+    return tile_rows > 8 ? (masked ? 3 : 4) : (masked ? 4 : 6);
+}
+
+constexpr long long kSms = 148;
+
+// Splits of a sequence's keys at most; tiles = sequences x kv heads x row tiles.
+int dp8_auto_splits(long long tiles, int Lk, int d, int tile_rows, bool masked) {
+    // at least 256 keys to a split (the kernel keeps to that by each sequence's own length)
     const long long most = (static_cast<long long>(Lk) + DP8_MIN_BLOCKS * DP8_BLOCK - 1) / (DP8_MIN_BLOCKS * DP8_BLOCK);
-    S = S > 64 ? 64 : S;
+    const long long room = kSms * dp8_resident(d, tile_rows, masked) / tiles;  // splits that fit the GPU at once
+    long long S;
+    if (room >= 2 && (Lk <= 8192 || room < 16)) {
+        // one wave, merged inside clusters: 9.9 us for one sequence of 4097 keys and 8 heads, 27.7 for 24 sequences
+        // of up to 2049 keys and 16 heads of 64 (31-36 in 3 and more splits)
+        S = room < DP8_MAX_CLUSTER ? room : DP8_MAX_CLUSTER;
+    } else {
+        // about 2.9 waves, so that uneven sequences even out, without many short splits: 32 x 32768 keys, 8 heads:
+        // 344-355 us at 5-16 splits, 361-370 at 3-4, 369-379 at 24-32; 32 sequences of 1-8192 keys 62-63 us at 4-6
+        // splits, 66 at 3, 70-107 at 12-32
+        S = (1280 + tiles / 2) / tiles;
+        S = S > 64 ? 64 : S;
+    }
     S = S > most ? most : S;
     return static_cast<int>(S < 1 ? 1 : S);
 }
 
-size_t dp8_workspace(long long rows, int S, int d) {
+// Of parts that go through memory.
+size_t parts_bytes(long long rows, int S, int d) {
     return S <= 1 ? 0 : static_cast<size_t>(rows) * S * (static_cast<size_t>(d) + 1) * sizeof(float);
 }
 
 template <int D, int NT, bool kMasked>
 int launch_dp8_kernel(const PagedFp8Params& p, unsigned grid, cudaStream_t s) {
-    decode_paged_fp8_kernel<D, NT, kMasked><<<grid, 32 * DP8_WARPS, Dp8Traits<D>::SMEM_BYTES, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(32 * DP8_WARPS);
+    cfg.dynamicSmemBytes = Dp8Traits<D>::SMEM_BYTES;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.S;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.cluster;
+    if (cudaLaunchKernelEx(&cfg, decode_paged_fp8_kernel<D, NT, kMasked>, p) != cudaSuccess) {
+        cudaGetLastError();
+        return FATTN_ERR_CUDA;
+    }
+    return FATTN_OK;
 }
 
 // A merge kernel, set up while the kernel before it runs.
@@ -90,16 +122,18 @@ int check_paged_fp8(const void* q, const void* k, const void* v, const float* ks
 // The split kernel over the rows of every sequence, and the merge.
 int launch_dp8(PagedFp8Params p, int d, int num_splits, void* workspace, size_t workspace_bytes, void* stream) {
     const long long rows = static_cast<long long>(p.max_q) * p.g;
-    const int tile_rows = dp8_tile_rows(rows);
+    const int tile_rows = dp8_tile_rows(rows, p.max_q > 1);
     const long long row_tiles = (rows + tile_rows - 1) / tile_rows;
     const long long tiles = static_cast<long long>(p.B) * p.Hkv * row_tiles;
     const int Lk = p.max_pages << p.page_shift;
-    p.S = num_splits > 0 ? num_splits : dp8_auto_splits(tiles, Lk);
+    const bool masked = p.max_q > 1;
+    p.S = num_splits > 0 ? num_splits : dp8_auto_splits(tiles, Lk, d, tile_rows, masked);
+    p.cluster = p.S > 1 && p.S <= DP8_MAX_CLUSTER && tiles * p.S <= kSms * dp8_resident(d, tile_rows, masked) ? 1 : 0;
     if (p.S > Lk) return FATTN_ERR_INVALID_ARG;
     if (tiles * p.S > 0x7fffffffLL || static_cast<long long>(p.B) * p.max_q * p.Hq > 0x7fffffffLL) return FATTN_ERR_UNSUPPORTED;
     p.row_tiles = static_cast<int>(row_tiles);
     const long long all_rows = static_cast<long long>(p.total_q) * p.Hq;
-    const size_t need = dp8_workspace(all_rows, p.S, d);
+    const size_t need = parts_bytes(all_rows, p.S, d);
     if (need > 0) {
         if (!workspace || workspace_bytes < need) return FATTN_ERR_WORKSPACE;
         if (!aligned16(workspace)) return FATTN_ERR_MISALIGNED;
@@ -111,7 +145,6 @@ int launch_dp8(PagedFp8Params p, int d, int num_splits, void* workspace, size_t 
     if (st != FATTN_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const unsigned grid = static_cast<unsigned>(tiles * p.S);
-    const bool masked = p.max_q > 1;
     if (d == 128) {
         if (tile_rows == 8) st = masked ? launch_dp8_kernel<128, 1, true>(p, grid, s) : launch_dp8_kernel<128, 1, false>(p, grid, s);
         else st = masked ? launch_dp8_kernel<128, 2, true>(p, grid, s) : launch_dp8_kernel<128, 2, false>(p, grid, s);
@@ -119,7 +152,7 @@ int launch_dp8(PagedFp8Params p, int d, int num_splits, void* workspace, size_t 
         if (tile_rows == 8) st = masked ? launch_dp8_kernel<64, 1, true>(p, grid, s) : launch_dp8_kernel<64, 1, false>(p, grid, s);
         else st = masked ? launch_dp8_kernel<64, 2, true>(p, grid, s) : launch_dp8_kernel<64, 2, false>(p, grid, s);
     }
-    if (st != FATTN_OK || p.S == 1) return st;
+    if (st != FATTN_OK || p.S == 1 || p.cluster) return st;
     const long long merge_grid = (static_cast<long long>(p.B) * p.max_q * p.Hq + 3) / 4;  // a warp per row
     return d == 128 ? launch_merge(merge_paged_fp8_kernel<128>, merge_grid, 128, s, p, tile_rows)
                     : launch_merge(merge_paged_fp8_kernel<64>, merge_grid, 128, s, p, tile_rows);
@@ -161,7 +194,7 @@ int ext_splits(long long items, long long tiles, long long rows, int d) {
 
 // The item counter, then the parts' (o, lse).
 constexpr size_t kExtCounterBytes = 16;
-size_t ext_workspace(long long rows, int S, int d) { return kExtCounterBytes + dp8_workspace(rows, S, d); }
+size_t ext_workspace(long long rows, int S, int d) { return kExtCounterBytes + parts_bytes(rows, S, d); }
 
 // The pool [num_pages * page_size, Hkv, d] of codes: boxes of box_rows keys of one head.
 int encode_map_pages(CUtensorMap* map, const void* base, int d, int Hkv, long long rows, int box_rows) {
@@ -309,7 +342,7 @@ int attn_append_paged_fp8(const void* k, const void* v, long long k_stride, long
     // about one wave of 64 an SM
     const int W = page_size >= 128 ? 8 : page_size / 16;
     long long chunk = (2LL * H * num_tokens * W + 64LL * di.num_sms - 1) / (64LL * di.num_sms);
-    p.chunk = static_cast<int>(chunk < 1 ? 1 : (chunk > 32 ? 32 : chunk));
+        p.chunk = static_cast<int>(chunk < 1 ? 1 : (chunk > page_size ? page_size : chunk));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (d == 128)
         return W == 1 ? launch_append<128, 1>(p, s) : W == 2 ? launch_append<128, 2>(p, s) : W == 4 ? launch_append<128, 4>(p, s) : launch_append<128, 8>(p, s);
@@ -319,8 +352,8 @@ int attn_append_paged_fp8(const void* k, const void* v, long long k_stride, long
 int attn_decode_paged_fp8_auto_splits(int B, int Hq, int Hkv, int Lk, int d) {
     if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Lk < 1 || (d != 64 && d != 128)) return FATTN_ERR_INVALID_ARG;
     const long long g = Hq / Hkv;
-    const int t = dp8_tile_rows(g);
-    return dp8_auto_splits(static_cast<long long>(B) * Hkv * ((g + t - 1) / t), Lk);
+    const int t = dp8_tile_rows(g, false);
+    return dp8_auto_splits(static_cast<long long>(B) * Hkv * ((g + t - 1) / t), Lk, d, t, false);
 }
 
 int attn_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
@@ -367,9 +400,8 @@ size_t attn_fwd_paged_fp8_workspace_bytes(int B, int total_q, int max_seqlen_q, 
     const long long rows = max_q * g, all = static_cast<long long>(total_q) * Hq;
     if (g <= 128 && ext_path(max_q, g))
         return ext_workspace(all, ext_splits(static_cast<long long>(B) * Hkv * ext_pairs(max_q, g), (static_cast<long long>(Lk) + 127) / 128, all, d), d);
-    const int t = dp8_tile_rows(rows);
-    const int S = dp8_auto_splits(static_cast<long long>(B) * Hkv * ((rows + t - 1) / t), Lk);
-    return dp8_workspace(all, S, d);
+    const int t = dp8_tile_rows(rows, max_q > 1);
+    return parts_bytes(all, dp8_auto_splits(static_cast<long long>(B) * Hkv * ((rows + t - 1) / t), Lk, d, t, max_q > 1), d);
 }
 
 int attn_fwd_paged_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,

@@ -18,7 +18,7 @@
 // as warps (decode steps) each warp takes runs of its own.  The first 16 rows of
 // a warp (d = 128) stay in registers between the two passes, the rest is read
 // again from L2.  chunk grows from 1 (a decode step, too few tokens to fill the
-// GPU) to 32 (a prefill, where most tokens start no run).
+// GPU) to a page (a prefill, where most tokens start no run).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -48,16 +48,17 @@ __device__ __forceinline__ float pow2_scale(uint32_t amax_bits) {
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// Eight bf16 to eight codes; an infinity or a NaN becomes e4m3's NaN (x - x is
-// 0 for a finite x and NaN otherwise).
+// Eight bf16 to eight codes.  kAll: an infinity or a NaN may be among them and
+// becomes e4m3's NaN (x - x is 0 for a finite x and NaN otherwise).
+template <bool kAll>
 __device__ __forceinline__ uint2 quantize8(const uint4& r, float inv) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
     float f[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const float a = __uint_as_float(w[e] << 16), b = __uint_as_float(w[e] & 0xFFFF0000u);
-        f[2 * e] = fmaf(a, inv, a - a);
-        f[2 * e + 1] = fmaf(b, inv, b - b);
+        f[2 * e] = kAll ? fmaf(a, inv, a - a) : a * inv;
+        f[2 * e + 1] = kAll ? fmaf(b, inv, b - b) : b * inv;
     }
     return make_uint2(pack_e4m3x4(f[0], f[1], f[2], f[3]), pack_e4m3x4(f[4], f[5], f[6], f[7]));
 }
@@ -151,38 +152,51 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) append_paged_fp8_kerne
         const long long r0 = w * RPS + lane / LPR;  // this lane's row in step 0
         const long long rstep = static_cast<long long>(warps) * RPS;
         uint4 hold[HOLD];
-        uint32_t amax = 0;  // the largest finite magnitude, as bf16 bits
+        uint32_t amax = 0;  // the largest magnitude, as two bf16; 0x7F80 and above: not a finite number
         auto take = [&](const uint4& v) {
+            amax = __vmaxu2(amax, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                           __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+        };
+        auto take_finite = [&](const uint4& v) {
             const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
             for (int e = 0; e < 4; ++e) {
-                uint32_t a = u[e] & 0x7FFF7FFFu;
-                a &= ~__vcmpgeu2(a, 0x7F807F80u);
-                amax = __vmaxu2(amax, a);
+                const uint32_t lo = u[e] & 0x7FFFu, hi = (u[e] >> 16) & 0x7FFFu;
+                amax = lo < 0x7F80u && lo > amax ? lo : amax;
+                amax = hi < 0x7F80u && hi > amax ? hi : amax;
             }
+        };
+        auto row = [&](long long r) { return __ldg(reinterpret_cast<const uint4*>(x + (t + r) * stride)); };
+        // the largest over the lanes of the run's warps
+        auto over_unit = [&](uint32_t v) {
+            v = __reduce_max_sync(0xffffffffu, v);
+            if (WARPS > 1 && warps > 1) {
+                __syncthreads();  // the reads of the time before
+                if (lane == 0) sm_amax[warp] = v;
+                __syncthreads();
+#pragma unroll
+                for (int k = 0; k < WARPS; ++k) v = sm_amax[k] > v ? sm_amax[k] : v;
+            } else {
+                __syncwarp();
+            }
+            return v;
         };
 #pragma unroll
         for (int i = 0; i < HOLD; ++i) {
             const long long r = r0 + i * rstep;
             hold[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < n) hold[i] = __ldg(reinterpret_cast<const uint4*>(x + (t + r) * stride));
+            if (r < n) hold[i] = row(r);
         }
         // the scale before: read by every thread, written by one after the barrier below
         const float s_old = first > 0 ? scales[page * p.H] : 0.f;
 #pragma unroll
         for (int i = 0; i < HOLD; ++i) take(hold[i]);
-        for (long long r = r0 + HOLD * rstep; r < n; r += rstep)
-            take(__ldg(reinterpret_cast<const uint4*>(x + (t + r) * stride)));
-        amax = __vmaxu2(amax, amax >> 16) & 0xFFFFu;
-        amax = __reduce_max_sync(0xffffffffu, amax);
-        if (WARPS > 1 && warps > 1) {
-            __syncthreads();  // the previous run's reads of sm_amax
-            if (lane == 0) sm_amax[warp] = amax;
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < WARPS; ++k) amax = sm_amax[k] > amax ? sm_amax[k] : amax;
-        } else {
-            __syncwarp();
+        for (long long r = r0 + HOLD * rstep; r < n; r += rstep) take(row(r));
+        amax = over_unit((amax >> 16) > (amax & 0xFFFFu) ? amax >> 16 : amax & 0xFFFFu);
+        const bool all = amax >= 0x7F80u;  // infinities or NaN among the rows: the largest finite one
+        if (all) {
+            amax = 0;
+            for (long long r = r0; r < n; r += rstep) take_finite(row(r));
+            amax = over_unit(amax);
         }
         const float s = fmaxf(s_old, pow2_scale(amax << 16));
         const float inv = __frcp_rn(s);
@@ -205,7 +219,7 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) append_paged_fp8_kerne
                     if (__ldg(p.slots + t + i) == slot) return;
                 at = slot & page_mask;
             }
-            *reinterpret_cast<uint2*>(page_rows + at * row_bytes) = quantize8(v, inv);
+            *reinterpret_cast<uint2*>(page_rows + at * row_bytes) = all ? quantize8<true>(v, inv) : quantize8<false>(v, inv);
         };
 #pragma unroll
         for (int i = 0; i < HOLD; ++i) {
@@ -213,20 +227,22 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) append_paged_fp8_kerne
             if (r < n) put(r, hold[i]);
         }
         for (long long r = r0 + HOLD * rstep; r < n; r += rstep)
-            put(r, __ldg(reinterpret_cast<const uint4*>(x + (t + r) * stride)));
+            put(r, row(r));
     };
 
-    // the tokens of the chunk that start a run (the same in every warp)
-    bool start = false;
-    if (t_lo + lane < t_hi) {
-        const long long page = page_of(t_lo + lane);
-        start = page >= 0 && (t_lo + lane == 0 || page_of(t_lo + lane - 1) != page);
-    }
-    unsigned starts = __ballot_sync(0xffffffffu, start);
-    const bool own = __popc(starts) >= WARPS;
-    for (int k = 0; starts != 0; starts &= starts - 1, ++k) {
-        if (own && k % WARPS != warp) continue;
-        do_run(t_lo + __ffs(starts) - 1, own ? 0 : warp, own ? 1 : WARPS);
+    for (long long t32 = t_lo; t32 < t_hi; t32 += 32) {
+        // the tokens of these 32 that start a run (the same in every warp)
+        bool start = false;
+        if (t32 + lane < t_hi) {
+            const long long page = page_of(t32 + lane);
+            start = page >= 0 && (t32 + lane == 0 || page_of(t32 + lane - 1) != page);
+        }
+        unsigned starts = __ballot_sync(0xffffffffu, start);
+        const bool own = __popc(starts) >= WARPS;
+        for (int k = 0; starts != 0; starts &= starts - 1, ++k) {
+            if (own && k % WARPS != warp) continue;
+            do_run(t32 + __ffs(starts) - 1, own ? 0 : warp, own ? 1 : WARPS);
+        }
     }
 }
 
