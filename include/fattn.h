@@ -454,7 +454,7 @@ int attn_decode_paged_fp8_auto_splits(int B, int Hq, int Hkv, int Lk, int d);
  *   causal, window_left, window_right: the mask of attn_fwd per sequence
  *                 (bottom-right aligned: the last query sits at the last key)
  *   workspace     device scratch of attn_fwd_paged_fp8_workspace_bytes bytes,
- *                 16-byte aligned (may be NULL when that is 0)
+ *                 32-byte aligned (may be NULL when that is 0)
  * Offsets and lengths are clamped so that no access leaves the tensors.
  * Precision and key rows outside the mask as attn_decode_paged_fp8; a row
  * with no allowed key gets O = 0 and LSE = -inf.

@@ -44,6 +44,23 @@
 
 namespace fattn {
 
+constexpr int EXT_MIN_TILES = 4;  // key tiles of the smallest part: 512 keys
+
+// One item: a pair of row tiles of one sequence and kv head, and a part of the
+// key tiles they visit.  The loading warp works it out and hands it to the other
+// roles through shared memory.
+struct alignas(16) ExtItem {
+    int item;                     // its number, -1: there are no more
+    int b, h;
+    int split, active;            // this part, and the parts that hold tiles
+    int q0, n, len;               // first token, tokens and keys of the sequence
+    int tok[2], tok_end[2];       // tokens of the tiles
+    int lo_t[2], hi_t[2], lo, hi; // their key tiles, and the union
+    int full_lo[2], full_hi[2];   // keys every row of a tile may see
+    int k_lo, k_hi;               // keys that some row of the pair may see
+};
+constexpr int EXT_ITEM_BYTES = sizeof(ExtItem);
+
 template <int D>
 struct ExtTraits {
     static constexpr int THREADS = 384;
@@ -60,8 +77,9 @@ struct ExtTraits {
     // kv_full, kv_empty[NSTAGE]; v16_full, v16_empty, q_full, s_full, p_ready, o_full, item_full, item_empty[2];
     // sc_full, sc_empty[SCALE_SLOTS]; drain
     static constexpr int NBAR = 2 * NSTAGE + 16 + 2 * SCALE_SLOTS + 1;
-    static constexpr int SMEM_MISC_OFF = SMEM_BAR_OFF + NBAR * 8;
-    // misc words: TMEM address, abort flag, items[2], NaN rounds[4] (an item is dealt once every
+    static constexpr int SMEM_ITEM_OFF = (SMEM_BAR_OFF + NBAR * 8 + 15) / 16 * 16;  // two ExtItem
+    static constexpr int SMEM_MISC_OFF = SMEM_ITEM_OFF + 2 * EXT_ITEM_BYTES;
+    // misc words: TMEM address, abort flag, unused[2], NaN rounds[4] (an item is dealt once every
     // role has read the item two rounds before it, so a round's entry outlives its epilogue)
     static constexpr int SMEM_BYTES = SMEM_MISC_OFF + 32 + 1024;  // + alignment slack
     static_assert(SMEM_BYTES <= 232448, "shared memory");
@@ -78,6 +96,7 @@ struct ExtParams {
     int n_pairs, n_items;   // pairs of row tiles per sequence at most; B * Hkv * n_pairs * splits
     int box_rows;           // keys per TMA box: min(page_size, 128)
     int splits;             // parts that an item's key tiles are cut into at most
+    int o_vec32;            // o is 32-byte aligned: rows are written 32 bytes at a time
 };
 
 // Instruction descriptor of kind::f16 with f16 A and B (format 0), fp32 D.
@@ -89,20 +108,6 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn, int
 // Matrix descriptor of 64-byte rows with 64-byte swizzle (eight rows are 512
 // bytes), layout 4 in bits 61-63.
 constexpr uint32_t kSdescHiSw64Sbo512 = (512u >> 4) | (1u << 14) | (4u << 29);
-
-constexpr int EXT_MIN_TILES = 4;  // key tiles of the smallest part: 512 keys
-
-// One item: a pair of row tiles of one sequence and kv head, and a part of the
-// key tiles they visit.
-struct ExtItem {
-    int b, h;
-    int split, active;            // this part, and the parts that hold tiles
-    int q0, n, len;               // first token, tokens and keys of the sequence
-    int tok[2], tok_end[2];       // tokens of the tiles
-    int lo_t[2], hi_t[2], lo, hi; // their key tiles, and the union
-    int full_lo[2], full_hi[2];   // keys every row of a tile may see
-    int k_lo, k_hi;               // keys that some row of the pair may see
-};
 
 // Keys [lo, hi) of token i, as key_range.
 __device__ __forceinline__ void ext_keys(const PagedFp8Params& c, int n, int len, int i, int* lo, int* hi) {
@@ -117,6 +122,7 @@ __device__ __forceinline__ void ext_keys(const PagedFp8Params& c, int n, int len
 
 __device__ __forceinline__ ExtItem ext_pair(const ExtParams& p, int b, int h, int pair, int split) {
     ExtItem it;
+    it.item = 0;
     it.b = b;
     it.h = h;
     it.split = split;
@@ -179,7 +185,9 @@ __device__ __forceinline__ ExtItem ext_pair(const ExtParams& p, int b, int h, in
 __device__ __forceinline__ ExtItem ext_item(const ExtParams& p, int item) {
     const int split = item % p.splits, pb = item / p.splits;
     const int bh = pb / p.n_pairs;
-    return ext_pair(p, bh / p.c.Hkv, bh % p.c.Hkv, p.n_pairs - 1 - pb % p.n_pairs, split);
+    ExtItem it = ext_pair(p, bh / p.c.Hkv, bh % p.c.Hkv, p.n_pairs - 1 - pb % p.n_pairs, split);
+    it.item = item;
+    return it;
 }
 
 // Whether some row of a tile that visits key tile j may not see all of it.
@@ -273,7 +281,7 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t misc = base + T::SMEM_MISC_OFF;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(gbase + T::SMEM_MISC_OFF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + T::SMEM_MISC_OFF + 4);
-    const uint32_t item_ring = misc + 8;
+    ExtItem* items = reinterpret_cast<ExtItem*>(gbase + T::SMEM_ITEM_OFF);
     volatile int* nan_round = reinterpret_cast<volatile int*>(gbase + T::SMEM_MISC_OFF + 16);
     int* status = &g_fattn_status;
 
@@ -320,14 +328,15 @@ __global__ void __launch_bounds__(384, 1)
         const bool ok = mbar_wait(bar, parity, abort_flag, status, -6);
         return __all_sync(0xffffffffu, ok) != 0;
     };
-    // The item of a round, from the producer's two-entry ring (whole warps).
-    auto next_item = [&](int round, int* item) {
+    // The item of a round, from the loading warp's two entries (whole warps): false
+    // if there are no more.
+    auto next_item = [&](int round, ExtItem& it) {
         const int e = round & 1;
         if (!warp_wait(item_full0 + 8 * e, (round >> 1) & 1)) return false;
-        *item = lds_s32(item_ring + 4u * e);
+        it = items[e];
         __syncwarp();
         if (lane == 0) mbar_arrive(item_empty0 + 8 * e);
-        return *item >= 0;
+        return it.item >= 0;
     };
 
     if (warp < 4) {
@@ -346,16 +355,18 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 if (item >= p.n_items || item < 0) item = -1;
                 const int e = round & 1;
+                ExtItem it{};
+                if (item >= 0) it = ext_item(p, item);
+                else it.item = -1;
                 if (round >= 2) {
                     ok = warp_wait(item_empty0 + 8 * e, ((round >> 1) - 1) & 1);
                     if (!ok) break;
                 }
                 if (lane == 0) {
-                    sts_s32(item_ring + 4u * e, item);
+                    items[e] = it;
                     mbar_arrive(item_full0 + 8 * e);
                 }
                 if (item < 0) break;
-                const ExtItem it = ext_item(p, item);
                 // lanes 0-7: the page of their box; lanes 8-15: of their 16-key block
                 const int mine = lane < 8 ? lane * p.box_rows : (lane & 7) * 16;
                 int page = it.lo < it.hi && lane < 16 ? ext_page(p.c, it.b, static_cast<long long>(it.lo) * 128 + mine) : 0;
@@ -414,10 +425,9 @@ __global__ void __launch_bounds__(384, 1)
                     const int e = round & 1;
                     ok = mbar_wait(item_full0 + 8 * e, (round >> 1) & 1, abort_flag, status, -6);
                     if (!ok) break;
-                    const int item = lds_s32(item_ring + 4u * e);
+                    const ExtItem it = items[e];
                     mbar_arrive(item_empty0 + 8 * e);
-                    if (item < 0) break;
-                    const ExtItem it = ext_item(p, item);
+                    if (it.item < 0) break;
                     const uint32_t ring0 = ring, v16_0 = v16;
                     bool q_seen[2] = {false, false};
                     for (int j = it.lo; j <= it.hi && it.lo < it.hi && ok; ++j) {
@@ -480,9 +490,8 @@ __global__ void __launch_bounds__(384, 1)
             uint32_t ring = 1, v16 = 0;  // V tiles take the odd slots
             bool ok = true;
             for (int round = 0; ok; ++round) {
-                int item;
-                if (!next_item(round, &item)) break;
-                const ExtItem it = ext_item(p, item);
+                ExtItem it;
+                if (!next_item(round, it)) break;
                 for (int j = it.lo; j < it.hi; ++j, ring += 2, ++v16) {
                     const uint32_t slot = ring % T::NSTAGE, buf = v16 & 1u;
                     ok = warp_wait(kv_full0 + 8 * slot, (ring / T::NSTAGE) & 1u);
@@ -504,26 +513,30 @@ __global__ void __launch_bounds__(384, 1)
                             const int q = (2 * c) & 7;
                             sts_f16x16(row + ((q ^ (r & 7)) << 4), row + (((q + 1) ^ (r & 7)) << 4), v);
                         };
+                        const uint32_t keep = seen ? 0xFFFFFFFFu : 0u;
                         uint32_t hit = 0;  // bit 7 of every byte: a NaN code
                         if (edge) {
-#pragma unroll 2
+#pragma unroll 1
                             for (int c = 0; c < D / 16; ++c) {
                                 const uint4 v = lds_u4(code_at(c));
                                 hit |= ((v.x & 0x7F7F7F7Fu) + 0x01010101u) | ((v.y & 0x7F7F7F7Fu) + 0x01010101u) |
                                        ((v.z & 0x7F7F7F7Fu) + 0x01010101u) | ((v.w & 0x7F7F7F7Fu) + 0x01010101u);
                             }
-                            hit &= 0x80808080u;
+                            hit &= 0x80808080u & keep;
                         }
-                        if (!edge || (seen && hit == 0)) {
+                        if (!__any_sync(0xffffffffu, hit != 0)) {
 #pragma unroll
-                            for (int c = 0; c < D / 16; ++c) put(c, lds_u4(code_at(c)));
+                            for (int c = 0; c < D / 16; ++c) {
+                                const uint4 v = lds_u4(code_at(c));
+                                put(c, make_uint4(v.x & keep, v.y & keep, v.z & keep, v.w & keep));
+                            }
                         } else {
 #pragma unroll 1
                             for (int c = 0; c < D / 16; ++c) {
-                                const uint4 v = seen ? lds_u4(code_at(c)) : make_uint4(0u, 0u, 0u, 0u);
-                                put(c, make_uint4(drop_nan4(v.x), drop_nan4(v.y), drop_nan4(v.z), drop_nan4(v.w)));
+                                const uint4 v = lds_u4(code_at(c));
+                                put(c, make_uint4(drop_nan4(v.x & keep), drop_nan4(v.y & keep), drop_nan4(v.z & keep), drop_nan4(v.w & keep)));
                             }
-                            nan |= seen;
+                            nan |= hit != 0;
                         }
                     }
                     if (nan) nan_round[round & 3] = round + 1;
@@ -559,60 +572,59 @@ __global__ void __launch_bounds__(384, 1)
         long long q_row = 0;                  // row (token, query head) of q and o
         float my = 0.f, l = 0.f;
         for (int round = 0; ok; ++round) {
-            int n_item;
-            const bool have = next_item(round, &n_item);
-            int n_tok = 0, n_split = 0, n_active = 0, lo = 0, hi = 0, lo_u = 0, hi_u = 0, full_lo = 0, full_hi = 0, key_lo = 0, key_hi = 0;
+            ExtItem it;
+            const bool have = next_item(round, it);
+            int n_tok = 0, lo = 0, hi = 0, full_lo = 0, full_hi = 0, key_lo = 0, key_hi = 0;
             bool n_valid = false;
             long long n_row = 0;
             float n_c = 0.f;
             if (have) {
-                const ExtItem it = ext_item(p, n_item);
-                n_tok = it.tok[t] + tok_of_row;
-                n_valid = tok_of_row < p.toks && n_tok < it.tok_end[t];
-                n_split = it.split;
-                n_active = it.active;
-                lo = it.lo_t[t], hi = it.hi_t[t], lo_u = it.lo, hi_u = it.hi;
-                full_lo = it.full_lo[t], full_hi = it.full_hi[t];
+                const int tok0 = t == 0 ? it.tok[0] : it.tok[1], tok1 = t == 0 ? it.tok_end[0] : it.tok_end[1];
+                lo = t == 0 ? it.lo_t[0] : it.lo_t[1], hi = t == 0 ? it.hi_t[0] : it.hi_t[1];
+                full_lo = t == 0 ? it.full_lo[0] : it.full_lo[1], full_hi = t == 0 ? it.full_hi[0] : it.full_hi[1];
+                n_tok = tok0 + tok_of_row;
+                n_valid = tok_of_row < p.toks && n_tok < tok1;
                 if (n_valid) ext_keys(p.c, it.n, it.len, n_tok, &key_lo, &key_hi);
                 n_row = (static_cast<long long>(it.q0) + n_tok) * p.c.Hq + static_cast<long long>(it.h) * p.c.g + head_of_row;
                 if (lo < hi) {
-                    // this thread's query row as two e4m3 terms; the tile's products of the item before are done
-                    uint4 raw_q[D / 8];
-                    uint32_t ab = 0;  // the largest magnitude as bf16 bits: an infinity or a NaN is above every number
+                    // The warp's 32 query rows as two e4m3 terms each, RPL rows at a time with 16 bytes
+                    // to a lane: whole rows per load (a thread loading its own row touches 32 lines per
+                    // instruction, 2.4 us an item).  The tile's products of the item before are done.
+                    constexpr int LPR = D / 8, RPL = 32 / LPR;
+                    const int sub = lane / LPR, v = lane % LPR;
+                    int e2_mine = 0;
+#pragma unroll 4
+                    for (int i = 0; i < 32; i += RPL) {
+                        const long long src = __shfl_sync(0xffffffffu, n_row, i + sub);
+                        const bool there = __shfl_sync(0xffffffffu, n_valid ? 1 : 0, i + sub) != 0;
+                        const uint4 x = there ? __ldg(reinterpret_cast<const uint4*>(p.c.q + src * D) + v) : make_uint4(0u, 0u, 0u, 0u);
+                        // the largest magnitude as bf16 bits: an infinity or a NaN is above every number
+                        uint32_t ab = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
 #pragma unroll
-                    for (int v = 0; v < D / 8; ++v)
-                        raw_q[v] = n_valid ? __ldg(reinterpret_cast<const uint4*>(p.c.q + n_row * D) + v) : make_uint4(0u, 0u, 0u, 0u);
+                        for (int o = LPR / 2; o > 0; o >>= 1) ab = __vmaxu2(ab, __shfl_xor_sync(0xffffffffu, ab, o));
+                        ab = (ab >> 16) > (ab & 0xFFFFu) ? ab >> 16 : ab & 0xFFFFu;
+                        // the row's largest magnitude <= 448 * 2^e2, e2 within [-100, 120]
+                        int e2 = static_cast<int>(ab >> 7) - 127 - 8 + ((ab & 0x7Fu) > 0x60u ? 1 : 0);
+                        e2 = e2 < -100 ? -100 : (e2 > 120 ? 120 : e2);
+                        const float down = ab >= 0x7F80u ? CUDART_NAN_F : pow2f(-e2);  // a row that is not finite becomes NaN
+                        const int e2_of = __shfl_sync(0xffffffffu, e2, (lane % RPL) * LPR);
+                        if (lane / RPL == i / RPL) e2_mine = e2_of;
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                        uint32_t h8[4], l8[4];
 #pragma unroll
-                    for (int v = 0; v < D / 8; ++v)
-                        ab = __vmaxu2(ab, __vmaxu2(__vmaxu2(raw_q[v].x & 0x7FFF7FFFu, raw_q[v].y & 0x7FFF7FFFu),
-                                                   __vmaxu2(raw_q[v].z & 0x7FFF7FFFu, raw_q[v].w & 0x7FFF7FFFu)));
-                    ab = (ab >> 16) > (ab & 0xFFFFu) ? ab >> 16 : ab & 0xFFFFu;
-                    // the row's largest magnitude <= 448 * 2^e2, e2 within [-100, 120]
-                    int e2 = static_cast<int>(ab >> 7) - 127 - 8 + ((ab & 0x7Fu) > 0x60u ? 1 : 0);
-                    e2 = e2 < -100 ? -100 : (e2 > 120 ? 120 : e2);
-                    const float down = ab >= 0x7F80u ? CUDART_NAN_F : pow2f(-e2);  // a row that is not finite becomes NaN
-                    n_c = p.c.scale_log2 * pow2f(e2);
-#pragma unroll
-                    for (int v = 0; v < D / 8; ++v) {
-                        const uint32_t w[4] = {raw_q[v].x, raw_q[v].y, raw_q[v].z, raw_q[v].w};
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
+                        for (int k = 0; k < 4; ++k)
                             // f16 holds the scaled bf16 exactly (down to 2^-24), and so the difference
-                            split_f16x2(pack_f16x2(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xFFFF0000u) * down), hi[i], lo[i]);
+                            split_f16x2(pack_f16x2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down), h8[k], l8[k]);
                         // 8 bytes of each term, in 128-byte rows swizzled by row % 8
-                        const uint32_t q_base = sQ + t * T::Q_BYTES + row * 128 + (v & 1) * 8;
-                        const uint32_t h0 = hi[0] | (hi[1] << 16), h1 = hi[2] | (hi[3] << 16);
-                        const uint32_t l0 = lo[0] | (lo[1] << 16), l1 = lo[2] | (lo[3] << 16);
-                        if constexpr (D == 128) {
-                            const uint32_t at = q_base + (((v >> 1) ^ (row & 7)) << 4);
-                            sts_u2(at, h0, h1);
-                            sts_u2(at + 128 * 128, l0, l1);
-                        } else {
-                            sts_u2(q_base + (((v >> 1) ^ (row & 7)) << 4), h0, h1);
-                            sts_u2(q_base + (((4 + (v >> 1)) ^ (row & 7)) << 4), l0, l1);
-                        }
+                        const int r = quarter * 32 + i + sub;
+                        const uint32_t q_base = sQ + t * T::Q_BYTES + r * 128 + (v & 1) * 8;
+                        const uint32_t hi_at = q_base + (((v >> 1) ^ (r & 7)) << 4);
+                        // d = 128: the terms are tiles of their own; d = 64: the halves of a row
+                        const uint32_t lo_at = D == 128 ? hi_at + 128 * 128 : q_base + (((4 + (v >> 1)) ^ (r & 7)) << 4);
+                        sts_u2(hi_at, h8[0] | (h8[1] << 16), h8[2] | (h8[3] << 16));
+                        sts_u2(lo_at, l8[0] | (l8[1] << 16), l8[2] | (l8[3] << 16));
                     }
+                    n_c = p.c.scale_log2 * pow2f(e2_mine);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(q_full0 + 8 * t);
@@ -662,14 +674,22 @@ __global__ void __launch_bounds__(384, 1)
                             }
                             if (part) {
 #pragma unroll
-                                for (int v = 0; v < 8; ++v)
-                                    reinterpret_cast<float4*>(wrow + ch * 32)[v] = make_float4(f[4 * v], f[4 * v + 1], f[4 * v + 2], f[4 * v + 3]);
-                            } else {
-#pragma unroll
                                 for (int v = 0; v < 4; ++v)
-                                    reinterpret_cast<uint4*>(orow + ch * 32)[v] =
-                                        make_uint4(pack_bf16x2(f[8 * v], f[8 * v + 1]), pack_bf16x2(f[8 * v + 2], f[8 * v + 3]),
-                                                   pack_bf16x2(f[8 * v + 4], f[8 * v + 5]), pack_bf16x2(f[8 * v + 6], f[8 * v + 7]));
+                                    stg256(wrow + ch * 32 + 8 * v, __float_as_uint(f[8 * v]), __float_as_uint(f[8 * v + 1]),
+                                           __float_as_uint(f[8 * v + 2]), __float_as_uint(f[8 * v + 3]), __float_as_uint(f[8 * v + 4]),
+                                           __float_as_uint(f[8 * v + 5]), __float_as_uint(f[8 * v + 6]), __float_as_uint(f[8 * v + 7]));
+                            } else {
+                                uint32_t o16[16];
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o16[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+                                if (p.o_vec32) {
+                                    stg256(orow + ch * 32, o16[0], o16[1], o16[2], o16[3], o16[4], o16[5], o16[6], o16[7]);
+                                    stg256(orow + ch * 32 + 16, o16[8], o16[9], o16[10], o16[11], o16[12], o16[13], o16[14], o16[15]);
+                                } else {
+#pragma unroll
+                                    for (int v = 0; v < 4; ++v)
+                                        reinterpret_cast<uint4*>(orow + ch * 32)[v] = make_uint4(o16[4 * v], o16[4 * v + 1], o16[4 * v + 2], o16[4 * v + 3]);
+                                }
                             }
                         }
                     }
@@ -684,7 +704,8 @@ __global__ void __launch_bounds__(384, 1)
                 }
             }
             if (!have) break;
-            item = n_item, tok = n_tok, split = n_split, active = n_active, round_of = round;
+            item = it.item, tok = n_tok, split = it.split, active = it.active, round_of = round;
+            const int lo_u = it.lo, hi_u = it.hi;
             valid = n_valid, visited = lo < hi, q_row = n_row, pending = true;
             const float c_row = n_c;
             my = -CUDART_INF_F;

@@ -193,7 +193,7 @@ int ext_splits(long long items, long long tiles, long long rows, int d) {
 }
 
 // The item counter, then the parts' (o, lse).
-constexpr size_t kExtCounterBytes = 16;
+constexpr size_t kExtCounterBytes = 32;
 size_t ext_workspace(long long rows, int S, int d) { return kExtCounterBytes + parts_bytes(rows, S, d); }
 
 // The pool [num_pages * page_size, Hkv, d] of codes: boxes of box_rows keys of one head.
@@ -239,13 +239,14 @@ int launch_ext(const PagedFp8Params& c, int d, long long pool_rows, void* worksp
     const long long n_items = items * p.splits;
     if (n_items > 0x7fff0000LL || items > 0x07ffffffLL || static_cast<long long>(c.B) * c.max_q * c.Hq > 0x7fffffffLL) return FATTN_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < ext_workspace(rows, p.splits, d)) return FATTN_ERR_WORKSPACE;
-    if (!aligned16(workspace)) return FATTN_ERR_MISALIGNED;
+    if (reinterpret_cast<uintptr_t>(workspace) & 31u) return FATTN_ERR_MISALIGNED;
     p.counter = static_cast<unsigned int*>(workspace);
     p.c.ws_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + kExtCounterBytes);
     p.c.ws_lse = p.c.ws_o + rows * p.splits * d;
     p.n_items = static_cast<int>(n_items);
     const int page_size = 1 << c.page_shift;
     p.box_rows = page_size < 128 ? page_size : 128;
+    p.o_vec32 = (reinterpret_cast<uintptr_t>(c.o) & 31u) == 0 ? 1 : 0;
     DeviceInfo di;
     int st = device_ready(&di);
     if (st != FATTN_OK) return st;
