@@ -93,9 +93,10 @@ struct ExtParams {
     PagedFp8Params c;       // the cache, the rows, the mask
     unsigned int* counter;  // zeroed before the launch: the next item to deal
     int toks;               // tokens per row tile: floor(128 / g)
-    int n_pairs, n_items;   // pairs of row tiles per sequence at most; B * Hkv * n_pairs * splits
+    int n_pairs, n_items;   // pairs of row tiles per sequence at most; items
+    int n_whole;            // pairs (in the items' order) that are one item; the others are `splits` items each
     int box_rows;           // keys per TMA box: min(page_size, 128)
-    int splits;             // parts that an item's key tiles are cut into at most
+    int splits;             // parts that a pair's key tiles are cut into at most
     int o_vec32;            // o is 32-byte aligned: rows are written 32 bytes at a time
 };
 
@@ -120,7 +121,7 @@ __device__ __forceinline__ void ext_keys(const PagedFp8Params& c, int n, int len
     *hi = h > l ? h : l;
 }
 
-__device__ __forceinline__ ExtItem ext_pair(const ExtParams& p, int b, int h, int pair, int split) {
+__device__ __forceinline__ ExtItem ext_pair(const ExtParams& p, int b, int h, int pair, int split, int splits) {
     ExtItem it;
     it.item = 0;
     it.b = b;
@@ -161,7 +162,7 @@ __device__ __forceinline__ ExtItem ext_pair(const ExtParams& p, int b, int h, in
         it.lo = it.hi = 0;
         return it;
     }
-    int per = (it.hi - it.lo + p.splits - 1) / p.splits;
+    int per = (it.hi - it.lo + splits - 1) / splits;
     per = per < EXT_MIN_TILES ? EXT_MIN_TILES : per;
     it.active = (it.hi - it.lo + per - 1) / per;
     if (it.active > 1) {
@@ -180,12 +181,17 @@ __device__ __forceinline__ ExtItem ext_pair(const ExtParams& p, int b, int h, in
     return it;
 }
 
-// Items run through the parts of a pair, the pairs of a sequence and head from
-// the last one (the longest under causal masking), and then the heads.
+// Pairs run through a sequence and head from its last one (the longest under
+// causal masking), then the heads; the last ones are cut into parts.
 __device__ __forceinline__ ExtItem ext_item(const ExtParams& p, int item) {
-    const int split = item % p.splits, pb = item / p.splits;
+    int pb = item, split = 0, splits = 1;
+    if (item >= p.n_whole) {
+        splits = p.splits;
+        pb = p.n_whole + (item - p.n_whole) / splits;
+        split = (item - p.n_whole) % splits;
+    }
     const int bh = pb / p.n_pairs;
-    ExtItem it = ext_pair(p, bh / p.c.Hkv, bh % p.c.Hkv, p.n_pairs - 1 - pb % p.n_pairs, split);
+    ExtItem it = ext_pair(p, bh / p.c.Hkv, bh % p.c.Hkv, p.n_pairs - 1 - pb % p.n_pairs, split, splits);
     it.item = item;
     return it;
 }
@@ -832,10 +838,9 @@ __global__ void __launch_bounds__(384, 1)
 template <int D>
 __global__ void __launch_bounds__(256) merge_ext_kernel(const __grid_constant__ ExtParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int x = blockIdx.x >> 4;
-    const int bh = x / p.n_pairs, pair = x % p.n_pairs;
-    const int h = bh % p.c.Hkv;
-    const ExtItem it = ext_pair(p, bh / p.c.Hkv, h, pair, 0);
+    const int pb = p.n_whole + (blockIdx.x >> 4);
+    const int bh = pb / p.n_pairs, h = bh % p.c.Hkv;
+    const ExtItem it = ext_pair(p, bh / p.c.Hkv, h, p.n_pairs - 1 - pb % p.n_pairs, 0, p.splits);
     if (it.active <= 1) return;
     const int rows = (it.tok_end[1] - it.tok[0]) * p.c.g;
 #pragma unroll

@@ -172,18 +172,21 @@ long long ext_pairs(long long max_q, int g) {
     return ((max_q + toks - 1) / toks + 1) / 2;
 }
 
-// Parts of an item's key tiles: the count with the shortest time by a model of
-// the kernel, whole rounds of one item per SM.  Measured on B200: 2.1 us a key
-// tile, 8 us more an item, 5 us for the merge and 1.6 TB/s for the parts' (o, lse).  16 items over 64 tiles: 47 us in 8 parts, 62 in 10, 64 in 16; 128 items
-// over 16 tiles: 52 us whole, 57 in 2 parts, 64 in 3.
-int ext_splits(long long items, long long tiles, long long rows, int d) {
-    const double sms = 148.0;
+// How the pairs of row tiles become items: the whole rounds of one pair per SM
+// stay whole, the pairs of the last, incomplete round are cut into parts of the
+// keys where a model of the kernel's time says so.  Measured on B200: 2.0 us a
+// key tile, 8 us more an item, 5 us for the merge and 1.6 TB/s for the parts'
+// (o, lse).  16 pairs over 64 tiles: 47 us in 8 parts, 62 in 10, 64 in 16; 128
+// pairs over 16 tiles: 52 us whole, 57 in 2 parts, 64 in 3.
+int ext_splits(long long pairs, long long tiles, int toks, int g, int d) {
+    const long long tail = pairs % kSms;
+    const double part_bytes = static_cast<double>(tail) * 2 * toks * g * (d + 1) * 8;
     int best = 1;
     double least = 0.0;
     for (int S = 1; S <= 32 && (S == 1 || static_cast<long long>(S) * EXT_MIN_TILES <= tiles); ++S) {
-        const double rounds = std::ceil(static_cast<double>(items) * S / sms);
-        double us = rounds * (std::ceil(static_cast<double>(tiles) / S) * 2.1 + 8.0);
-        if (S > 1) us += 5.0 + static_cast<double>(rows) * S * (d + 1) * 8 / 1.6e6;
+        const double rounds = std::ceil(static_cast<double>(tail) * S / kSms);
+        double us = rounds * (std::ceil(static_cast<double>(tiles) / S) * 2.0 + 8.0);
+        if (S > 1) us += 5.0 + part_bytes * S / 1.6e6;
         if (S == 1 || us < least) {
             least = us;
             best = S;
@@ -226,18 +229,19 @@ int launch_ext(const PagedFp8Params& c, int d, long long pool_rows, void* worksp
     p.c = c;
     p.toks = 128 / c.g;
     p.n_pairs = static_cast<int>(ext_pairs(c.max_q, c.g));
-    const long long items = static_cast<long long>(c.B) * c.Hkv * p.n_pairs;
+    const long long pairs = static_cast<long long>(c.B) * c.Hkv * p.n_pairs;
     const long long rows = static_cast<long long>(c.total_q) * c.Hq;
     const long long all_tiles = ((static_cast<long long>(c.max_pages) << c.page_shift) + 127) / 128;
-    p.splits = ext_splits(items, all_tiles, rows, d);  // what the workspace is sized for
+    p.splits = ext_splits(pairs, all_tiles, p.toks, c.g, d);  // what the workspace is sized for
     if (c.window_left >= 0 && (c.causal || c.window_right >= 0)) {
         // a pair of row tiles sees the window and its own tokens
         const long long seen = (static_cast<long long>(c.window_left) + (c.causal ? 0 : c.window_right) + 2LL * p.toks + 255) / 128;
-        const int S = ext_splits(items, seen < all_tiles ? seen : all_tiles, rows, d);
+        const int S = ext_splits(pairs, seen < all_tiles ? seen : all_tiles, p.toks, c.g, d);
         p.splits = S < p.splits ? S : p.splits;
     }
-    const long long n_items = items * p.splits;
-    if (n_items > 0x7fff0000LL || items > 0x07ffffffLL || static_cast<long long>(c.B) * c.max_q * c.Hq > 0x7fffffffLL) return FATTN_ERR_UNSUPPORTED;
+    p.n_whole = static_cast<int>(p.splits == 1 ? pairs : pairs - pairs % kSms);
+    const long long cut = pairs - p.n_whole, n_items = p.n_whole + cut * p.splits;
+    if (pairs > 0x07ffffffLL || static_cast<long long>(c.B) * c.max_q * c.Hq > 0x7fffffffLL) return FATTN_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < ext_workspace(rows, p.splits, d)) return FATTN_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 31u) return FATTN_ERR_MISALIGNED;
     p.counter = static_cast<unsigned int*>(workspace);
@@ -265,7 +269,7 @@ int launch_ext(const PagedFp8Params& c, int d, long long pool_rows, void* worksp
     else attn_paged_fp8_kernel<64><<<grid, ExtTraits<64>::THREADS, ExtTraits<64>::SMEM_BYTES, s>>>(mk, mv, p);
     if (cudaGetLastError() != cudaSuccess) return FATTN_ERR_CUDA;
     if (p.splits == 1) return FATTN_OK;
-    return d == 128 ? launch_merge(merge_ext_kernel<128>, 16 * items, 256, s, p) : launch_merge(merge_ext_kernel<64>, 16 * items, 256, s, p);
+    return d == 128 ? launch_merge(merge_ext_kernel<128>, 16 * cut, 256, s, p) : launch_merge(merge_ext_kernel<64>, 16 * cut, 256, s, p);
 }
 
 template <int D, int WARPS>
@@ -400,7 +404,7 @@ size_t attn_fwd_paged_fp8_workspace_bytes(int B, int total_q, int max_seqlen_q, 
     const int g = Hq / Hkv;
     const long long rows = max_q * g, all = static_cast<long long>(total_q) * Hq;
     if (g <= 128 && ext_path(max_q, g))
-        return ext_workspace(all, ext_splits(static_cast<long long>(B) * Hkv * ext_pairs(max_q, g), (static_cast<long long>(Lk) + 127) / 128, all, d), d);
+        return ext_workspace(all, ext_splits(static_cast<long long>(B) * Hkv * ext_pairs(max_q, g), (static_cast<long long>(Lk) + 127) / 128, 128 / g, g, d), d);
     const int t = dp8_tile_rows(rows, max_q > 1);
     return parts_bytes(all, dp8_auto_splits(static_cast<long long>(B) * Hkv * ((rows + t - 1) / t), Lk, d, t, max_q > 1), d);
 }
