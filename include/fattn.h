@@ -425,7 +425,7 @@ int attn_append_paged_fp8(const void* k, const void* v, long long k_stride, long
  * element), probabilities are rounded to f16 (2^-11 of each), sums and
  * statistics are fp32, O is rounded to bf16 once.  Key rows outside the attended
  * range have no effect, whatever their codes are (NaN included).  The V scales
- * of one sequence may differ by up to 2^80; one below 2^-100 counts as 2^-100.
+ * of one sequence may differ by up to 2^80; one below 2^-80 counts as 2^-80.
  */
 int attn_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
                           const float* k_scales, const float* v_scales,
@@ -456,8 +456,11 @@ int attn_decode_paged_fp8_auto_splits(int B, int Hq, int Hkv, int Lk, int d);
  *   workspace     device scratch of attn_fwd_paged_fp8_workspace_bytes bytes,
  *                 32-byte aligned (may be NULL when that is 0)
  * Offsets and lengths are clamped so that no access leaves the tensors.
- * Precision and key rows outside the mask as attn_decode_paged_fp8; a row
- * with no allowed key gets O = 0 and LSE = -inf.
+ * Precision and key rows outside the mask as attn_decode_paged_fp8, but for
+ * the query rows of sequences with max_seqlen_q * Hq / Hkv > 48: they enter the
+ * products as the sum of two e4m3 terms, exact down to 2^-10 of the row's
+ * largest element and off by up to 2^-18 of it below (a row with an infinity or
+ * a NaN gets NaN).  A row with no allowed key gets O = 0 and LSE = -inf.
  */
 int attn_fwd_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
                        const float* k_scales, const float* v_scales,

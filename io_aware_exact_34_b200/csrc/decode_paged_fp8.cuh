@@ -69,7 +69,7 @@ constexpr int DP8_ROUND_BLOCKS = 4;  // a split's blocks: as many for each warp
 constexpr int DP8_MAX_CLUSTER = 8;  // splits that merge inside a cluster
 constexpr float kDp8Shift = 7.f;    // p' = 2^(y - my + 7)
 constexpr float kDp8Slack = 8.f;
-constexpr float kMinValueScale = 7.888609052210118e-31f;  // 2^-100: smaller V scales count as this
+constexpr float kMinValueScale = 8.271806125530277e-25f;  // 2^-80: smaller V scales count as this, so that sums of p' / vs stay finite
 
 struct PagedFp8Params {
     const __nv_bfloat16* q;     // rows (token, query head) of d elements

@@ -35,6 +35,7 @@ struct DeviceInfo {
     bool ready = false;
     bool sm100 = false;
     bool fwd_regs_ok = false;  // the prefill kernels' register pool covers their split
+    bool ext_regs_ok = false;  // and the paged 8-bit prefill's
     int num_sms = 0;
 };
 
@@ -54,6 +55,18 @@ bool fwd_register_pool_ok() {
     const long long need = 128LL * T::REGS_LOW + 256LL * T::REGS_HIGH;
     return static_cast<long long>(a.numRegs) * T::THREADS >= need && static_cast<long long>(b.numRegs) * T::THREADS >= need &&
            static_cast<long long>(c.numRegs) * T::THREADS >= need;
+}
+
+// The same for the paged 8-bit prefill.
+template <int D>
+bool ext_register_pool_ok() {
+    cudaFuncAttributes a;
+    if (cudaFuncGetAttributes(&a, attn_paged_fp8_kernel<D>) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    using T = ExtTraits<D>;
+    return static_cast<long long>(a.numRegs) * T::THREADS >= 128LL * T::REGS_LOW + 256LL * T::REGS_HIGH;
 }
 
 std::mutex g_mutex;
@@ -142,6 +155,7 @@ int device_ready(DeviceInfo* out) {
                 return FATTN_ERR_CUDA;
             }
             di.fwd_regs_ok = fwd_register_pool_ok<128>() && fwd_register_pool_ok<64>();
+            di.ext_regs_ok = ext_register_pool_ok<128>() && ext_register_pool_ok<64>();
             if (g_encode == nullptr) {
                 void* fn = nullptr;
                 cudaDriverEntryPointQueryResult q;

@@ -211,19 +211,6 @@ int encode_map_pages(CUtensorMap* map, const void* base, int d, int Hkv, long lo
     return r == CUDA_SUCCESS ? FATTN_OK : FATTN_ERR_CUDA;
 }
 
-// The kernel's warpgroups change their register budgets: the compiled count
-// has to provide the pool, or the raising ones would wait forever.
-template <int D>
-bool ext_register_pool_ok() {
-    cudaFuncAttributes a;
-    if (cudaFuncGetAttributes(&a, attn_paged_fp8_kernel<D>) != cudaSuccess) {
-        cudaGetLastError();
-        return false;
-    }
-    using T = ExtTraits<D>;
-    return static_cast<long long>(a.numRegs) * T::THREADS >= 128LL * T::REGS_LOW + 256LL * T::REGS_HIGH;
-}
-
 int launch_ext(const PagedFp8Params& c, int d, long long pool_rows, void* workspace, size_t workspace_bytes, void* stream) {
     ExtParams p{};
     p.c = c;
@@ -241,7 +228,7 @@ int launch_ext(const PagedFp8Params& c, int d, long long pool_rows, void* worksp
     }
     p.n_whole = static_cast<int>(p.splits == 1 ? pairs : pairs - pairs % kSms);
     const long long cut = pairs - p.n_whole, n_items = p.n_whole + cut * p.splits;
-    if (pairs > 0x07ffffffLL || static_cast<long long>(c.B) * c.max_q * c.Hq > 0x7fffffffLL) return FATTN_ERR_UNSUPPORTED;
+    if (pairs > 0x07ffffffLL) return FATTN_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < ext_workspace(rows, p.splits, d)) return FATTN_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 31u) return FATTN_ERR_MISALIGNED;
     p.counter = static_cast<unsigned int*>(workspace);
@@ -254,7 +241,7 @@ int launch_ext(const PagedFp8Params& c, int d, long long pool_rows, void* worksp
     DeviceInfo di;
     int st = device_ready(&di);
     if (st != FATTN_OK) return st;
-    if (!(d == 128 ? ext_register_pool_ok<128>() : ext_register_pool_ok<64>())) return FATTN_ERR_UNSUPPORTED;
+    if (!di.ext_regs_ok) return FATTN_ERR_UNSUPPORTED;
     CUtensorMap mk, mv;
     if (encode_map_pages(&mk, c.k, d, c.Hkv, pool_rows, p.box_rows) != FATTN_OK ||
         encode_map_pages(&mv, c.v, d, c.Hkv, pool_rows, p.box_rows) != FATTN_OK)

@@ -402,6 +402,9 @@ FWD_CASES = [
     ([20, 0, 3], [50, 7, 3], 16, 4, 2, 128, {}), ([20, 5], [50, 9], 16, 2, 1, 64, dict(left=3)), ([5], [300], 16, 4, 1, 128, dict(causal=False, right=2)),
     ([600, 80], [256, 80], 128, 16, 4, 128, dict(behind=5)), ([600, 80], [256, 20], 16, 4, 2, 128, dict(most=33)),
     ([900], [300], 16, 4, 2, 128, dict(spread=20)),
+    # few rows: sequences without keys, rows behind the last sequence, splits
+    ([0, 30, 0], [2, 3, 0], 16, 4, 2, 128, dict(behind=4)), ([5000, 3], [4, 2], 16, 8, 2, 128, {}), ([9000], [3], 64, 4, 1, 64, dict(left=5000)),
+    ([700, 20], [6, 6], 32, 4, 1, 128, dict(most=4)),
     # keys in several parts, some of them without a key for some rows
     ([3000, 700, 5], [100, 64, 5], 16, 8, 2, 128, {}), ([2500], [40], 64, 8, 1, 64, dict(left=900)),
     ([2100, 1300], [70, 70], 32, 4, 4, 128, dict(causal=False)), ([2600], [33], 16, 16, 4, 64, dict(causal=False, left=700, right=300)),
@@ -454,6 +457,60 @@ def test_fwd_rejects(fl):
     for bad in (dict(max_seqlen_q=0), dict(scale=0.0)):
         with pytest.raises(fl.FattnError):
             call(**bad)
+
+
+def test_value_scale_of_nothing(fl):
+    """V scales far below every other, and of 0: their rows count as keys and add (next to) nothing."""
+    g = torch.Generator().manual_seed(23)
+    kc, vc, ks, vs = _cache(4, 16, 1, 128, g)
+    q = torch.randn(1, 2, 1, 128, generator=g).to(torch.bfloat16)
+    for tiny in (0.0, 2.0 ** -140, 2.0 ** -60):
+        small = vs.clone()
+        small[1:3] = tiny
+        for v in (small, torch.full_like(vs, tiny)):
+            exp = ref.attention(q[0, :, 0].double()[None], ref.gather(ref.value(kc), ks.double(), [0, 1, 2, 3], 60),
+                                ref.gather(ref.value(vc), v.double(), [0, 1, 2, 3], 60), float(torch.tensor(128 ** -0.5, dtype=torch.float32)))
+            args = (kc.cuda(), vc.cuda(), ks.cuda(), v.cuda(), _i32([[0, 1, 2, 3]]), _i32([60]))
+            o, lse = fl.attn_decode_paged_fp8(q.cuda(), *args)
+            assert bool(((o[:, :, 0].double().cpu() - exp[0]).abs() <= ref.tolerances(*[exp[i] for i in (0, 2, 3)], 128, 60)[0] + 2.0 ** -70).all())
+            assert bool(((lse.double().cpu() - exp[1]).abs() <= ref.tolerances(*[exp[i] for i in (0, 2, 3)], 128, 60)[1]).all())
+
+
+def test_buffers_given(fl):
+    """Outputs and workspaces of the caller's: the same results as with the library's choice."""
+    g = torch.Generator().manual_seed(24)
+    lens, new, page, hq, hkv, d = [3000, 700], [40, 2], 16, 8, 2, 128
+    pages = sum(-(-x // page) for x in lens) + 4
+    table = _table(lens, page, 200, pages, g)
+    cache = [t.cuda() for t in _cache(pages, page, hkv, d, g)]
+    q = torch.randn(2, hq, 1, d, generator=g).to(torch.bfloat16).cuda()
+    for S in (0, 1, 3, 12):
+        a = fl.attn_decode_paged_fp8(q, *cache, _i32(table), _i32(lens), num_splits=S)
+        ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+        o, lse = torch.empty_like(q), torch.empty(2, hq, device="cuda")
+        b = fl.attn_decode_paged_fp8(q, *cache, _i32(table), _i32(lens), num_splits=S, o=o, lse=lse, workspace=ws)
+        assert b[0] is o and b[1] is lse and torch.equal(a[0], o) and torch.equal(a[1], lse)
+    for n in ([40, 2], [3, 2]):
+        x = torch.randn(sum(n), hq, d, generator=g).to(torch.bfloat16).cuda()
+        cu = _i32([0, n[0], sum(n)])
+        a = fl.attn_fwd_paged_fp8(x, *cache, _i32(table), _i32(lens), cu, max(n), causal=True)
+        ws = torch.empty(fl.attn_fwd_paged_fp8_workspace_bytes(2, sum(n), max(n), hq, hkv, 200 * page, d), dtype=torch.uint8, device="cuda")
+        o, lse = torch.empty_like(x), torch.empty(hq, sum(n), device="cuda")
+        b = fl.attn_fwd_paged_fp8(x, *cache, _i32(table), _i32(lens), cu, max(n), o=o, lse=lse, causal=True, workspace=ws)
+        assert b[0] is o and b[1] is lse and torch.equal(a[0], o) and torch.equal(a[1], lse)
+        with pytest.raises(fl.FattnError):
+            fl.attn_fwd_paged_fp8(x, *cache, _i32(table), _i32(lens), cu, max(n), causal=True, workspace=ws[:ws.numel() - 64])
+    free, held = _i32([pages - 1, pages - 2, pages - 3]), _i32(lens)
+    t1, t2 = _i32(table), _i32(table)
+    a = fl.attn_paged_plan(held, _i32(new), free, t1, page, 50)
+    bufs = [torch.empty_like(t) for t in a]
+    b = fl.attn_paged_plan(held, _i32(new), free, t2, page, 50, *bufs)
+    assert torch.equal(t1, t2) and all(x is y and torch.equal(x, z) for x, y, z in zip(b, bufs, a))
+    with pytest.raises(fl.FattnError):
+        fl.attn_paged_plan(held, _i32(new), free, t2, page, 50, seqlens_out=held)
+    for bad in (dict(slot_map=bufs[0][:49]), dict(cu_seqlens=bufs[1].long()), dict(counts=bufs[3][:1])):
+        with pytest.raises(ValueError):
+            fl.attn_paged_plan(held, _i32(new), free, t2, page, 50, **bad)
 
 
 # ---------------------------------------------------------------- as they are used
