@@ -46,11 +46,12 @@
 // warps (by the sequence's own length, not the table's width).  Where all CTAs
 // fit the GPU at once, up to 8 splits are the CTAs of one thread-block cluster
 // and combine their (o, lse) through distributed shared memory (one sequence of
-// 4097 keys: 9.9 us in 8 splits, 11.6 through the workspace, 10.2 in 16 splits).
+// 4097 keys: 9.6 us in 8 splits, 11.2 through the workspace, 10.6 in 16 splits).
 // Longer work goes through the workspace and a merge kernel that starts by
 // programmatic launch: there the heads of one key range stand next to each
-// other in the grid and read the same DRAM pages together (32 x 32768 keys: 344
-// us, 370-380 with the splits of a head next to each other).
+// other in the grid and read the same DRAM pages together (32 x 32768 keys: 320
+// us, 370-390 with the splits of a head, or one split of all sequences, next to
+// each other).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -154,7 +155,7 @@ __device__ __forceinline__ SplitSpan split_span(const PagedFp8Params& p, const S
 
 template <int D>
 struct Dp8Traits {
-    static constexpr int STAGES = 4;
+    static constexpr int STAGES = 3;
     static constexpr int VB = D / 8;                        // bytes of a V row per lane
     static constexpr int KV_BYTES = 2 * DP8_BLOCK * D;      // one step of one warp
     static constexpr int WARP_BYTES = STAGES * KV_BYTES;
@@ -274,10 +275,15 @@ __device__ __forceinline__ int row_exponent(float amax) {
     return e < -100 ? -100 : (e > 126 ? 126 : e);
 }
 
+// CTAs that an SM holds: 48 KB of ring at d = 128, 24 KB at 64, and registers.
+__host__ __device__ constexpr int dp8_resident(int d, int tile_rows, bool masked) {
+    return d == 128 ? (tile_rows > 8 ? (masked ? 2 : 3) : 4) : (tile_rows > 8 ? (masked ? 3 : 4) : (masked ? 4 : 6));
+}
+
 // NT tiles of 8 query rows per CTA.  kMasked: rows of the tile may see
 // different keys (more than one token per sequence).
 template <int D, int NT, bool kMasked>
-__global__ void __launch_bounds__(32 * DP8_WARPS, D == 64 && NT == 1 && !kMasked ? 6 : 1) decode_paged_fp8_kernel(const PagedFp8Params p) {
+__global__ void __launch_bounds__(32 * DP8_WARPS, dp8_resident(D, 8 * NT, kMasked)) decode_paged_fp8_kernel(const PagedFp8Params p) {
     using T = Dp8Traits<D>;
     constexpr int ROWS = 8 * NT;
     constexpr int HALVES = D / 64;

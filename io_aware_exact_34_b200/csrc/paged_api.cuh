@@ -27,30 +27,36 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 // 16; 48 rows: 39.4 and 36.9).
 int dp8_tile_rows(long long rows, bool masked) { return rows <= (masked ? 32 : 8) ? 8 : 16; }
 
-// CTAs of the split kernel that an SM holds (shared memory and registers).
-int dp8_resident(int d, int tile_rows, bool masked) {
-    if (d == 128) return masked && tile_rows > 8 ? 2 : 3;
-    return tile_rows > 8 ? (masked ? 3 : 4) : (masked ? 4 : 6);
-}
-
 constexpr long long kSms = 148;
 
-// Splits of a sequence's keys at most; tiles = sequences x kv heads x row tiles.
-int dp8_auto_splits(long long tiles, int Lk, int d, int tile_rows, bool masked) {
+// Splits of a sequence's keys at most; tiles = sequences x kv heads x row tiles,
+// keys = the most that a row sees.
+int dp8_auto_splits(long long tiles, int keys, int d, int tile_rows, bool masked) {
     // at least 256 keys to a split (the kernel keeps to that by each sequence's own length)
-    const long long most = (static_cast<long long>(Lk) + DP8_MIN_BLOCKS * DP8_BLOCK - 1) / (DP8_MIN_BLOCKS * DP8_BLOCK);
-    const long long room = kSms * dp8_resident(d, tile_rows, masked) / tiles;  // splits that fit the GPU at once
-    long long S;
-    if (room >= 2 && (Lk <= 8192 || room < 16)) {
-        // one wave, merged inside clusters: 9.9 us for one sequence of 4097 keys and 8 heads, 27.7 for 24 sequences
-        // of up to 2049 keys and 16 heads of 64 (31-36 in 3 and more splits)
+    const long long most = (static_cast<long long>(keys) + DP8_MIN_BLOCKS * DP8_BLOCK - 1) / (DP8_MIN_BLOCKS * DP8_BLOCK);
+    const long long slots = kSms * dp8_resident(d, tile_rows, masked), room = slots / tiles;  // splits that fit the GPU at once
+    long long S = 1;
+    if (room >= 2 && keys <= (room < 16 ? 16384 : 8192)) {
+        // one wave, merged inside clusters: 9.6 us for one sequence of 4097 keys and 8 heads (room 74), 58 for 32
+        // sequences of 1-8192 keys (room 2; 61-64 in 3 to 9 splits through the workspace), 27 for 24 sequences in a
+        // window of 2048 keys with 16 heads of 64 (room 2; 29-37)
         S = room < DP8_MAX_CLUSTER ? room : DP8_MAX_CLUSTER;
+    } else if (room >= 8) {
+        // one wave: 8192 keys, 32 rows (room 18): 18 us in 18 splits, 25 in 40
+        S = room < 64 ? room : 64;
     } else {
-        // about 2.9 waves, so that uneven sequences even out, without many short splits: 32 x 32768 keys, 8 heads:
-        // 344-355 us at 5-16 splits, 361-370 at 3-4, 369-379 at 24-32; 32 sequences of 1-8192 keys 62-63 us at 4-6
-        // splits, 66 at 3, 70-107 at 12-32
-        S = (1280 + tiles / 2) / tiles;
-        S = S > 64 ? 64 : S;
+        // several waves with as little as possible left over in the last one, 2048 keys or more to a split: 32 x 32768
+        // keys, 8 heads (592 slots, 256 CTAs a split): 340-347 us at 4, 9 and 16 splits, 351-363 at 6, 7 and 12, 387 at 5
+        const long long limit = keys / 2048 < 4 ? 4 : (keys / 2048 > 16 ? 16 : keys / 2048);
+        double best = 0.0;
+        for (long long k = 1; k <= limit; ++k) {
+            const double waves = static_cast<double>(tiles * k) / static_cast<double>(slots);
+            const double use = waves / std::ceil(waves) - 0.004 * static_cast<double>(k);
+            if (use > best) {
+                best = use;
+                S = k;
+            }
+        }
     }
     S = S > most ? most : S;
     return static_cast<int>(S < 1 ? 1 : S);
@@ -127,7 +133,13 @@ int launch_dp8(PagedFp8Params p, int d, int num_splits, void* workspace, size_t 
     const long long tiles = static_cast<long long>(p.B) * p.Hkv * row_tiles;
     const int Lk = p.max_pages << p.page_shift;
     const bool masked = p.max_q > 1;
-    p.S = num_splits > 0 ? num_splits : dp8_auto_splits(tiles, Lk, d, tile_rows, masked);
+    int keys = Lk;
+    if (p.window_left >= 0 && (p.causal || p.window_right >= 0)) {
+        const long long seen = 1LL + p.window_left + (p.causal ? 0 : p.window_right);
+        keys = seen < Lk ? static_cast<int>(seen) : Lk;
+    }
+    // fewer keys never mean more splits, so that a workspace sized without the window suffices
+    p.S = num_splits > 0 ? num_splits : dp8_auto_splits(tiles, keys, d, tile_rows, masked);
     p.cluster = p.S > 1 && p.S <= DP8_MAX_CLUSTER && tiles * p.S <= kSms * dp8_resident(d, tile_rows, masked) ? 1 : 0;
     if (p.S > Lk) return FATTN_ERR_INVALID_ARG;
     if (tiles * p.S > 0x7fffffffLL || static_cast<long long>(p.B) * p.max_q * p.Hq > 0x7fffffffLL) return FATTN_ERR_UNSUPPORTED;
