@@ -602,50 +602,45 @@ __global__ void __launch_bounds__(384, 1)
                 if (lo < hi) {
                     // The warp's 32 query rows as two e4m3 terms each, RPL rows at a time with 16 bytes
                     // to a lane: whole rows per load (a thread loading its own row touches 32 lines per
-                    // instruction, 2.4 us an item).  The tile's products of the item before are done.
+                    // instruction).  The tile's products of the item before are done.
                     constexpr int LPR = D / 8, RPL = 32 / LPR;
                     const int sub = lane / LPR, v = lane % LPR;
                     int e2_mine = 0;
-                    constexpr int BATCH = 8;  // loads in flight
-#pragma unroll 1
-                    for (int i0 = 0; i0 < 32; i0 += BATCH * RPL) {
-                        uint4 raw_q[BATCH];
+                    uint4 raw_q[LPR];  // all of them in flight
 #pragma unroll
-                        for (int k = 0; k < BATCH; ++k) {
-                            const long long src = __shfl_sync(0xffffffffu, n_row, i0 + k * RPL + sub);
-                            const bool there = __shfl_sync(0xffffffffu, n_valid ? 1 : 0, i0 + k * RPL + sub) != 0;
-                            raw_q[k] = there ? __ldg(reinterpret_cast<const uint4*>(p.c.q + src * D) + v) : make_uint4(0u, 0u, 0u, 0u);
-                        }
+                    for (int k = 0; k < LPR; ++k) {
+                        const long long src = __shfl_sync(0xffffffffu, n_row, k * RPL + sub);
+                        const bool there = __shfl_sync(0xffffffffu, n_valid ? 1 : 0, k * RPL + sub) != 0;
+                        raw_q[k] = there ? __ldg(reinterpret_cast<const uint4*>(p.c.q + src * D) + v) : make_uint4(0u, 0u, 0u, 0u);
+                    }
 #pragma unroll
-                        for (int kk = 0; kk < BATCH; ++kk) {
-                            const int i = i0 + kk * RPL;
-                            const uint4 x = raw_q[kk];
-                            // the largest magnitude as bf16 bits: an infinity or a NaN is above every number
-                            uint32_t ab = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+                    for (int i = 0; i < 32; i += RPL) {
+                        const uint4 x = raw_q[i / RPL];
+                        // the largest magnitude as bf16 bits: an infinity or a NaN is above every number
+                        uint32_t ab = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
 #pragma unroll
-                            for (int o = LPR / 2; o > 0; o >>= 1) ab = __vmaxu2(ab, __shfl_xor_sync(0xffffffffu, ab, o));
-                            ab = (ab >> 16) > (ab & 0xFFFFu) ? ab >> 16 : ab & 0xFFFFu;
-                            // the row's largest magnitude <= 448 * 2^e2, e2 within [-100, 120]
-                            int e2 = static_cast<int>(ab >> 7) - 127 - 8 + ((ab & 0x7Fu) > 0x60u ? 1 : 0);
-                            e2 = e2 < -100 ? -100 : (e2 > 120 ? 120 : e2);
-                            const float down = ab >= 0x7F80u ? CUDART_NAN_F : pow2f(-e2);  // a row that is not finite becomes NaN
-                            const int e2_of = __shfl_sync(0xffffffffu, e2, (lane % RPL) * LPR);
-                            if (lane / RPL == i / RPL) e2_mine = e2_of;
-                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                            uint32_t h8[4], l8[4];
+                        for (int o = LPR / 2; o > 0; o >>= 1) ab = __vmaxu2(ab, __shfl_xor_sync(0xffffffffu, ab, o));
+                        ab = (ab >> 16) > (ab & 0xFFFFu) ? ab >> 16 : ab & 0xFFFFu;
+                        // the row's largest magnitude <= 448 * 2^e2, e2 within [-100, 120]
+                        int e2 = static_cast<int>(ab >> 7) - 127 - 8 + ((ab & 0x7Fu) > 0x60u ? 1 : 0);
+                        e2 = e2 < -100 ? -100 : (e2 > 120 ? 120 : e2);
+                        const float down = ab >= 0x7F80u ? CUDART_NAN_F : pow2f(-e2);  // a row that is not finite becomes NaN
+                        const int e2_of = __shfl_sync(0xffffffffu, e2, (lane % RPL) * LPR);
+                        if (lane / RPL == i / RPL) e2_mine = e2_of;
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                        uint32_t h8[4], l8[4];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                // f16 holds the scaled bf16 exactly (down to 2^-24), and so the difference
-                                split_f16x2(pack_f16x2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down), h8[k], l8[k]);
-                            // 8 bytes of each term, in 128-byte rows swizzled by row % 8
-                            const int r = quarter * 32 + i + sub;
-                            const uint32_t q_base = sQ + t * T::Q_BYTES + r * 128 + (v & 1) * 8;
-                            const uint32_t hi_at = q_base + (((v >> 1) ^ (r & 7)) << 4);
-                            // d = 128: the terms are tiles of their own; d = 64: the halves of a row
-                            const uint32_t lo_at = D == 128 ? hi_at + 128 * 128 : q_base + (((4 + (v >> 1)) ^ (r & 7)) << 4);
-                            sts_u2(hi_at, h8[0] | (h8[1] << 16), h8[2] | (h8[3] << 16));
-                            sts_u2(lo_at, l8[0] | (l8[1] << 16), l8[2] | (l8[3] << 16));
-                        }
+                        for (int k = 0; k < 4; ++k)
+                            // f16 holds the scaled bf16 exactly (down to 2^-24), and so the difference
+                            split_f16x2(pack_f16x2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down), h8[k], l8[k]);
+                        // 8 bytes of each term, in 128-byte rows swizzled by row % 8
+                        const int r = quarter * 32 + i + sub;
+                        const uint32_t q_base = sQ + t * T::Q_BYTES + r * 128 + (v & 1) * 8;
+                        const uint32_t hi_at = q_base + (((v >> 1) ^ (r & 7)) << 4);
+                        // d = 128: the terms are tiles of their own; d = 64: the halves of a row
+                        const uint32_t lo_at = D == 128 ? hi_at + 128 * 128 : q_base + (((4 + (v >> 1)) ^ (r & 7)) << 4);
+                        sts_u2(hi_at, h8[0] | (h8[1] << 16), h8[2] | (h8[3] << 16));
+                        sts_u2(lo_at, l8[0] | (l8[1] << 16), l8[2] | (l8[3] << 16));
                     }
                     n_c = p.c.scale_log2 * pow2f(e2_mine);
                     fence_proxy_async_smem();
