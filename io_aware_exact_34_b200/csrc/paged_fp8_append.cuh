@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) append_paged_fp8_kerne
     auto do_run = [&](long long t, int w, int warps) {
         const long long page = page_of(t);
         // the run's end, its lowest row, and whether its slots rise by one
-        long long n = 0;
+        int n = 0;  // at most T
         int first = 0x7fffffff;
         bool dense = true;
         long long before = 0;  // the slot of the token before the 32 in hand
@@ -149,8 +149,10 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) append_paged_fp8_kerne
         }
         dense = __all_sync(0xffffffffu, dense);
 
-        const long long r0 = w * RPS + lane / LPR;  // this lane's row in step 0
-        const long long rstep = static_cast<long long>(warps) * RPS;
+        const int r0 = w * RPS + lane / LPR;  // this lane's row in step 0
+        const int rstep = warps * RPS;
+        const __nv_bfloat16* x_row = x + (t + r0) * stride;
+        const long long x_step = rstep * stride;
         uint4 hold[HOLD];
         uint32_t amax = 0;  // the largest magnitude, as two bf16; 0x7F80 and above: not a finite number
         auto take = [&](const uint4& v) {
@@ -165,7 +167,7 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) append_paged_fp8_kerne
                 amax = hi < 0x7F80u && hi > amax ? hi : amax;
             }
         };
-        auto row = [&](long long r) { return __ldg(reinterpret_cast<const uint4*>(x + (t + r) * stride)); };
+        auto row = [&](int r) { return __ldg(reinterpret_cast<const uint4*>(x + (t + r) * stride)); };
         // the largest over the lanes of the run's warps
         auto over_unit = [&](uint32_t v) {
             v = __reduce_max_sync(0xffffffffu, v);
@@ -182,20 +184,19 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) append_paged_fp8_kerne
         };
 #pragma unroll
         for (int i = 0; i < HOLD; ++i) {
-            const long long r = r0 + i * rstep;
             hold[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < n) hold[i] = row(r);
+            if (r0 + i * rstep < n) hold[i] = __ldg(reinterpret_cast<const uint4*>(x_row + i * x_step));
         }
         // the scale before: read by every thread, written by one after the barrier below
         const float s_old = first > 0 ? scales[page * p.H] : 0.f;
 #pragma unroll
         for (int i = 0; i < HOLD; ++i) take(hold[i]);
-        for (long long r = r0 + HOLD * rstep; r < n; r += rstep) take(row(r));
+        for (int r = r0 + HOLD * rstep; r < n; r += rstep) take(row(r));
         amax = over_unit((amax >> 16) > (amax & 0xFFFFu) ? amax >> 16 : amax & 0xFFFFu);
         const bool all = amax >= 0x7F80u;  // infinities or NaN among the rows: the largest finite one
         if (all) {
             amax = 0;
-            for (long long r = r0; r < n; r += rstep) take_finite(row(r));
+            for (int r = r0; r < n; r += rstep) take_finite(row(r));
             amax = over_unit(amax);
         }
         const float s = fmaxf(s_old, pow2_scale(amax << 16));
@@ -204,30 +205,32 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) append_paged_fp8_kerne
         uint8_t* page_rows = pages + (page << shift) * row_bytes;
         if (first > 0 && s != s_old) {
             const float ratio = s_old * inv;
-            for (long long r = r0; r < first; r += rstep) {
+            for (int r = r0; r < first; r += rstep) {
                 uint2* q = reinterpret_cast<uint2*>(page_rows + r * row_bytes);
                 const uint2 c = *q;
                 *q = make_uint2(rescale4(c.x, ratio), rescale4(c.y, ratio));
             }
         }
-        auto put = [&](long long r, const uint4& v) {
-            long long at = first + r;
-            if (!dense) {
+        auto store = [&](uint8_t* at, const uint4& v) {
+            *reinterpret_cast<uint2*>(at) = all ? quantize8<true>(v, inv) : quantize8<false>(v, inv);
+        };
+        if (dense) {
+            uint8_t* at = page_rows + (first + r0) * row_bytes;
+            const long long step = rstep * row_bytes;
+#pragma unroll
+            for (int i = 0; i < HOLD; ++i)
+                if (r0 + i * rstep < n) store(at + i * step, hold[i]);
+            at += HOLD * step;
+            for (int r = r0 + HOLD * rstep; r < n; r += rstep, at += step) store(at, row(r));
+        } else {
+            for (int r = r0; r < n; r += rstep) {
                 // a slot named again by a later token of the run keeps that token's row
                 const long long slot = __ldg(p.slots + t + r);
-                for (long long i = r + 1; i < n; ++i)
-                    if (__ldg(p.slots + t + i) == slot) return;
-                at = slot & page_mask;
+                bool again = false;
+                for (int i = r + 1; i < n; ++i) again |= __ldg(p.slots + t + i) == slot;
+                if (!again) store(page_rows + (slot & page_mask) * row_bytes, row(r));
             }
-            *reinterpret_cast<uint2*>(page_rows + at * row_bytes) = all ? quantize8<true>(v, inv) : quantize8<false>(v, inv);
-        };
-#pragma unroll
-        for (int i = 0; i < HOLD; ++i) {
-            const long long r = r0 + i * rstep;
-            if (r < n) put(r, hold[i]);
         }
-        for (long long r = r0 + HOLD * rstep; r < n; r += rstep)
-            put(r, row(r));
     };
 
     for (long long t32 = t_lo; t32 < t_hi; t32 += 32) {
