@@ -142,7 +142,7 @@ int launch_dp8(PagedFp8Params p, int d, int num_splits, void* workspace, size_t 
     p.S = num_splits > 0 ? num_splits : dp8_auto_splits(tiles, keys, d, tile_rows, masked);
     p.cluster = p.S > 1 && p.S <= DP8_MAX_CLUSTER && tiles * p.S <= kSms * dp8_resident(d, tile_rows, masked) ? 1 : 0;
     if (p.S > Lk) return FATTN_ERR_INVALID_ARG;
-    if (tiles * p.S > 0x7fffffffLL || static_cast<long long>(p.B) * p.max_q * p.Hq > 0x7fffffffLL) return FATTN_ERR_UNSUPPORTED;
+    if (rows > 0x7fffff00LL || tiles * p.S > 0x7fffffffLL || static_cast<long long>(p.B) * p.max_q * p.Hq > 0x7fffffffLL) return FATTN_ERR_UNSUPPORTED;
     p.row_tiles = static_cast<int>(row_tiles);
     const long long all_rows = static_cast<long long>(p.total_q) * p.Hq;
     const size_t need = parts_bytes(all_rows, p.S, d);

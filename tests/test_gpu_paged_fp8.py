@@ -304,6 +304,21 @@ def test_decode_visible_nan(fl):
         assert torch.equal(lse.isnan().cpu(), want.all(-1)[..., 0])
 
 
+@pytest.mark.parametrize("new", [1, 40])
+def test_queries_that_are_not_finite(fl, new):
+    """An infinity or a NaN in a query row spoils that row and no other, in short and in long runs."""
+    g = torch.Generator().manual_seed(16)
+    kc, vc, ks, vs = [t.cuda() for t in _cache(8, 16, 2, 128, g)]
+    q = torch.randn(new, 4, 128, generator=g).to(torch.bfloat16)
+    clean = q.clone()
+    q[0, 1, 3], q[new - 1, 2, 100], q[new // 2, 0, 64] = math.inf, -math.inf, math.nan
+    bad = ~q.isfinite().all(-1)
+    a = fl.attn_fwd_paged_fp8(q.cuda(), kc, vc, ks, vs, _i32([list(range(8))]), _i32([100]), _i32([0, new]), new, causal=True)
+    b = fl.attn_fwd_paged_fp8(clean.cuda(), kc, vc, ks, vs, _i32([list(range(8))]), _i32([100]), _i32([0, new]), new, causal=True)
+    assert torch.equal(a[0].isnan().cpu(), bad[..., None].expand(q.shape)) and torch.equal(a[1].isnan().cpu(), bad.T)
+    assert torch.equal(a[0].cpu()[~bad], b[0].cpu()[~bad]) and torch.equal(a[1].T.cpu()[~bad], b[1].T.cpu()[~bad])
+
+
 def test_decode_bad_tables_and_lengths(fl):
     """Table entries outside the pool are clamped, lengths beyond the table too: same as with the clamped ones."""
     g = torch.Generator().manual_seed(13)
