@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(32 * DP8_WARPS, dp8_resident(D, 8 * NT, kMaske
     const uint8_t *k_lane = p.k + lane_off, *v_lane = p.v + lane_off;
     const long long copy_step = T::RPC * head_row;
     int table_lane = 0;  // lane i: the page of step 32*(issued/32) + i
-    auto issue = [&](int i, int stage) {
+    auto issue = [&](int i) {
         if ((i & 31) == 0) {
             const int mine = i + lane;
             if (mine < nsteps) {
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(32 * DP8_WARPS, dp8_resident(D, 8 * NT, kMaske
             const int off = (key_first + i * (DP8_WARPS * DP8_BLOCK)) & page_mask;
             const long long at = ((static_cast<long long>(page) << shift) + off) * head_row;
             const uint8_t *kp = k_lane + at, *vp = v_lane + at;
-            const uint32_t slot = ring + stage * T::KV_BYTES;
+            const uint32_t slot = ring + (i % T::STAGES) * T::KV_BYTES;
             const int rel = rel_of(i);
             if (rel >= 0 && rel + DP8_BLOCK <= k_len) {
 #pragma unroll
@@ -379,13 +379,13 @@ __global__ void __launch_bounds__(32 * DP8_WARPS, dp8_resident(D, 8 * NT, kMaske
                     vp += copy_step;
                 }
             }
-            const uint32_t sslot = sring + stage * 8;
+            const uint32_t sslot = sring + (i % T::STAGES) * 8;
             if (lane < 2) cp_async4(sslot + 4 * lane, (lane == 0 ? p.ks : p.vs) + static_cast<long long>(page) * p.Hkv + h);
         }
         cp_async_commit();
     };
 #pragma unroll
-    for (int i = 0; i < T::STAGES - 1; ++i) issue(i, i);
+    for (int i = 0; i < T::STAGES - 1; ++i) issue(i);
 
     // Q^T fragments: column r8 of tile nt, d in the order of the K fragments
     uint32_t qf[NT][HALVES][4][2];
@@ -455,12 +455,12 @@ __global__ void __launch_bounds__(32 * DP8_WARPS, dp8_resident(D, 8 * NT, kMaske
     }
 
 #pragma unroll 1
-    for (int i = 0, stage = 0; i < nsteps; ++i, stage = stage + 1 == T::STAGES ? 0 : stage + 1) {
+    for (int i = 0; i < nsteps; ++i) {
         cp_async_wait<T::STAGES - 2>();
         __syncwarp();  // a lane reads what others copied
-        issue(i + T::STAGES - 1, stage == 0 ? T::STAGES - 1 : stage - 1);  // the stage that the step before has read
-        const uint32_t slot = ring + stage * T::KV_BYTES;
-        const float2 sc = lds_f2(sring + stage * 8);
+        issue(i + T::STAGES - 1);
+        const uint32_t slot = ring + (i % T::STAGES) * T::KV_BYTES;
+        const float2 sc = lds_f2(sring + (i % T::STAGES) * 8);
         const int rel = rel_of(i);
 
         // S^T = K Q^T
