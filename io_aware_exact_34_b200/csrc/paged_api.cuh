@@ -45,15 +45,23 @@ int dp8_auto_splits(long long tiles, int keys, int d, int tile_rows, bool masked
         // one wave: 8192 keys, 32 rows (room 18): 18 us in 18 splits, 25 in 40
         S = room < 64 ? room : 64;
     } else {
-        // several waves with as little as possible left over in the last one, 2048 keys or more to a split: 32 x 32768
-        // keys, 8 heads (592 slots, 256 CTAs a split): 340-347 us at 4, 9 and 16 splits, 351-363 at 6, 7 and 12, 387 at 5
-        const long long limit = keys / 2048 < 4 ? 4 : (keys / 2048 > 16 ? 16 : keys / 2048);
+        // One wave whole or several in parts.  A CTA's time in keys: its share and a fixed part.  The lengths may all be
+        // the longest (whole waves count) or lie anywhere below it (the work balances, half a CTA's time stays over):
+        // the mean of both decides, and parts past one wave pay for the workspace.  Against the fullest last wave alone:
+        // 128 sequences of up to 2048 keys, 8 heads, 62 -> 56 us, all of 2048 keys 104 -> 92; 64 of up to 8192 keys
+        // 114 -> 101, all of 8192 keys 171 -> 181; 40 of up to 1024 keys with 4 tokens each 25.3 -> 20.7, full 45.5 ->
+        // 33.3.  32 x 32768 keys: 340-347 us at 4, 9 and 16 splits, 351-363 at 6, 7 and 12, 387 at 5.  More keys never
+        // give fewer splits: of two costs, each linear in the keys, the larger S has the larger constant.
+        const double fixed = tile_rows == 8 ? 200.0 : 500.0;
         double best = 0.0;
-        for (long long k = 1; k <= limit; ++k) {
+        for (int k = 1; k <= 16; ++k) {
             const double waves = static_cast<double>(tiles * k) / static_cast<double>(slots);
-            const double use = waves / std::ceil(waves) - 0.004 * static_cast<double>(k);
-            if (use > best) {
-                best = use;
+            const double share = static_cast<double>(keys) / k;
+            const double whole = std::ceil(waves) * (fixed + share);
+            const double ragged = waves <= 1.0 ? whole : waves * (fixed + 0.5 * share) + 0.5 * (fixed + share);
+            const double cost = whole + ragged + (waves > 1.0 && k > 1 ? 600.0 : 0.0);
+            if (k == 1 || cost < best) {
+                best = cost;
                 S = k;
             }
         }
