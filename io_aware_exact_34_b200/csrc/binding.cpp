@@ -205,10 +205,10 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
         need(q.size(2) == 1 && c.d == d && B > 0 && table.get_device() == place.dev && table.size(0) == B);
         const at::Tensor& lens = dense(a[6], at::kInt, {B}, place.dev);
         const int left = small(a[8]);
-        int S = small(a[9]);
+        const int splits = small(a[9]);
         const int64_t Lk = table.size(1) * c.page_size;
-        need(Lk > 0 && Lk <= kIntMax && S >= 0);
-        if (S == 0) S = g_splits(static_cast<int>(B), static_cast<int>(Hq), c.heads, static_cast<int>(Lk), static_cast<int>(d));
+        need(Lk > 0 && Lk <= kIntMax && splits >= 0);
+        const int S = splits ? splits : g_splits(static_cast<int>(B), static_cast<int>(Hq), c.heads, static_cast<int>(Lk), static_cast<int>(d));
         need(S > 0);
         const at::Tensor o = at::empty(q.sizes(), q.options()), lse = at::empty({B, Hq}, c.ks.options());
         const int64_t bytes = S > 1 ? 4 * B * Hq * S * (d + 1) : 0;
@@ -217,7 +217,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
         need(g_decode(q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), c.ks.data_ptr<float>(), c.vs.data_ptr<float>(),
                       table.data_ptr<int>(), static_cast<int>(table.size(1)), c.page_size, c.pages, o.data_ptr(),
                       lse.data_ptr<float>(), lens.data_ptr<int>(), static_cast<int>(B), static_cast<int>(Hq), c.heads,
-                      static_cast<int>(d), scale_of(a[7], d), left, S, bytes > 0 ? ws.data_ptr() : nullptr,
+                      static_cast<int>(d), scale_of(a[7], d), left, splits, bytes > 0 ? ws.data_ptr() : nullptr,
                       static_cast<size_t>(bytes), place.stream) == 0);
         return tuple(o, lse);
     });

@@ -528,6 +528,21 @@ def test_buffers_given(fl):
             fl.attn_paged_plan(held, _i32(new), free, t2, page, 50, **bad)
 
 
+def test_window_over_a_long_table(fl):
+    """The library splits what the window leaves, whoever brings the buffers: the same bits."""
+    g = torch.Generator().manual_seed(27)
+    lens, page, hq, hkv, d, width = [20000, 900], 16, 8, 2, 128, 2500
+    pages = sum(-(-x // page) for x in lens)
+    table = _i32(_table(lens, page, width, pages, g))
+    cache = [t.cuda() for t in _cache(pages, page, hkv, d, g)]
+    q = torch.randn(2, hq, 1, d, generator=g).to(torch.bfloat16).cuda()
+    for left in (-1, 5000, 40):
+        a = fl.attn_decode_paged_fp8(q, *cache, table, _i32(lens), window_left=left)
+        o, lse = torch.empty_like(q), torch.empty(2, hq, device="cuda")
+        fl.attn_decode_paged_fp8(q, *cache, table, _i32(lens), window_left=left, o=o, lse=lse)
+        assert torch.equal(a[0], o) and torch.equal(a[1], lse)
+
+
 # ---------------------------------------------------------------- as they are used
 def _serve(fl, steps, page, hq, hkv, d, seed):
     """A prompt batch, then decode steps, then drafted tokens: every step plans, appends and attends."""
