@@ -109,20 +109,14 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) append_paged_fp8_kerne
     float* scales = (kv ? p.scales[1] : p.scales[0]) + h;
     const long long row_bytes = static_cast<long long>(p.H) * D;
 
-    // page of a token, -1 for one that is not stored (a negative slot, or one beyond the pool)
-    auto page_of = [&](long long t) -> long long {
-        const long long s = __ldg(p.slots + t);
-        return s >= 0 && s < p.num_slots ? s >> shift : -1;
-    };
-
-    // One run of tokens from t on, by `warps` warps of which this one is `w`.
-    auto do_run = [&](long long t, int w, int warps) {
-        const long long page = page_of(t);
+    // One run of tokens from t (in slot0) on, by `warps` warps of which this one is `w`.
+    auto do_run = [&](long long t, long long slot0, int w, int warps) {
+        const long long page = slot0 >> shift;
+        const unsigned long long base = static_cast<unsigned long long>(page) << shift;
         // the run's end, its lowest row, and whether its slots rise by one
         int n = 0;  // at most T
-        int first = 0x7fffffff;
+        int first = static_cast<int>(slot0 & page_mask), low = first;
         bool dense = true;
-        long long before = 0;  // the slot of the token before the 32 in hand
         for (bool more = true; more;) {
             constexpr int AHEAD = 4;  // loads in flight: 128 tokens
             long long s[AHEAD];
@@ -134,20 +128,20 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) append_paged_fp8_kerne
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k) {
                 if (!more) break;
-                const unsigned in = __ballot_sync(0xffffffffu, s[k] >= 0 && s[k] < p.num_slots && (s[k] >> shift) == page);
-                const int m = in == 0xffffffffu ? 32 : __ffs(~in) - 1;
-                const int off = lane < m ? static_cast<int>(s[k] & page_mask) : 0x7fffffff;
-                long long prev = __shfl_up_sync(0xffffffffu, s[k], 1);
-                if (lane == 0) prev = n == 0 ? s[k] - 1 : before;
-                if (lane < m && s[k] != prev + 1) dense = false;
-                const int low = __reduce_min_sync(0xffffffffu, off);
-                first = low < first ? low : first;
-                before = __shfl_sync(0xffffffffu, s[k], 31);
+                const unsigned long long off = static_cast<unsigned long long>(s[k]) - base;  // in the page, or beyond its rows
+                const unsigned out = __ballot_sync(0xffffffffu, off >= (1ull << shift));
+                const int m = out == 0 ? 32 : __ffs(out) - 1;
+                const int row = static_cast<int>(off);
+                if (lane < m) {
+                    dense = dense && row == first + n + lane;
+                    low = row < low ? row : low;
+                }
                 n += m;
                 more = m == 32;
             }
         }
         dense = __all_sync(0xffffffffu, dense);
+        if (!dense) first = __reduce_min_sync(0xffffffffu, low);
 
         const int r0 = w * RPS + lane / LPR;  // this lane's row in step 0
         const int rstep = warps * RPS;
@@ -236,15 +230,19 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) append_paged_fp8_kerne
     for (long long t32 = t_lo; t32 < t_hi; t32 += 32) {
         // the tokens of these 32 that start a run (the same in every warp)
         bool start = false;
+        long long slot = -1;
         if (t32 + lane < t_hi) {
-            const long long page = page_of(t32 + lane);
-            start = page >= 0 && (t32 + lane == 0 || page_of(t32 + lane - 1) != page);
+            // stored (not a negative slot nor one beyond the pool), and in another page than the token before
+            slot = __ldg(p.slots + t32 + lane);
+            start = static_cast<unsigned long long>(slot) < static_cast<unsigned long long>(p.num_slots) &&
+                    (t32 + lane == 0 || (static_cast<unsigned long long>(slot ^ __ldg(p.slots + t32 + lane - 1)) >> shift) != 0);
         }
         unsigned starts = __ballot_sync(0xffffffffu, start);
         const bool own = __popc(starts) >= WARPS;
         for (int k = 0; starts != 0; starts &= starts - 1, ++k) {
             if (own && k % WARPS != warp) continue;
-            do_run(t32 + __ffs(starts) - 1, own ? 0 : warp, own ? 1 : WARPS);
+            const int at = __ffs(starts) - 1;
+            do_run(t32 + at, __shfl_sync(0xffffffffu, slot, at), own ? 0 : warp, own ? 1 : WARPS);
         }
     }
 }
