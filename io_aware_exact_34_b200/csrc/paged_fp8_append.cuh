@@ -16,8 +16,11 @@
 // It has a warp for every 16 rows of a page (1 to 8): where its runs are long
 // they share the rows of one run after the other, where there are as many runs
 // as warps (decode steps) each warp takes runs of its own.  The first 16 rows of
-// a warp (d = 128) stay in registers between the two passes, the rest is read
-// again from L2.  chunk grows from 1 (a decode step, too few tokens to fill the
+// a warp (d = 128) stay in registers between the two passes, the rest comes
+// again from L2, 16 rows in flight at once.  17.8k tokens of 8 heads of 128 take
+// 22, 23, 26, 30 and 30 us in pages of 16, 32, 64, 128 and 256 (16.7 for the
+// bytes alone): what is left is the chain of a run, slots -> rows -> maximum ->
+// codes, and 62 % of the issue slots.  chunk grows from 1 (a decode step, too few tokens to fill the
 // GPU) to a page (a prefill, where most tokens start no run).
 #pragma once
 
@@ -99,8 +102,8 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) append_paged_fp8_kerne
     // CTA = (chunk of tokens, head, K or V), K and V fastest
     const int kv = blockIdx.x & 1;
     const int h = (blockIdx.x >> 1) % p.H;
-    const long long t_lo = static_cast<long long>((blockIdx.x >> 1) / p.H) * p.chunk;
-    const long long t_hi = t_lo + p.chunk < p.T ? t_lo + p.chunk : p.T;
+    const unsigned int T = p.T, t_lo = (blockIdx.x >> 1) / p.H * p.chunk;
+    const unsigned int t_hi = T - t_lo < static_cast<unsigned int>(p.chunk) ? T : t_lo + p.chunk;
     const int shift = p.page_shift;
     const long long page_mask = (1LL << shift) - 1;
     const __nv_bfloat16* x = (kv ? p.x[1] : p.x[0]) + static_cast<long long>(h) * D + (lane % LPR) * 8;
@@ -110,7 +113,7 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) append_paged_fp8_kerne
     const long long row_bytes = static_cast<long long>(p.H) * D;
 
     // One run of tokens from t (in slot0) on, by `warps` warps of which this one is `w`.
-    auto do_run = [&](long long t, long long slot0, int w, int warps) {
+    auto do_run = [&](unsigned int t, long long slot0, int w, int warps) {
         const long long page = slot0 >> shift;
         const unsigned long long base = static_cast<unsigned long long>(page) << shift;
         // the run's end, its lowest row, and whether its slots rise by one
@@ -122,8 +125,8 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) append_paged_fp8_kerne
             long long s[AHEAD];
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k) {
-                const long long i = t + n + 32 * k + lane;
-                s[k] = i < p.T ? __ldg(p.slots + i) : -1;
+                const unsigned int i = t + n + 32 * k + lane;
+                s[k] = i < T ? __ldg(p.slots + i) : -1;
             }
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k) {
@@ -145,23 +148,9 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) append_paged_fp8_kerne
 
         const int r0 = w * RPS + lane / LPR;  // this lane's row in step 0
         const int rstep = warps * RPS;
-        const __nv_bfloat16* x_row = x + (t + r0) * stride;
+        const __nv_bfloat16* x_row = x + static_cast<long long>(t + r0) * stride;
         const long long x_step = rstep * stride;
         uint4 hold[HOLD];
-        uint32_t amax = 0;  // the largest magnitude, as two bf16; 0x7F80 and above: not a finite number
-        auto take = [&](const uint4& v) {
-            amax = __vmaxu2(amax, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                                           __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
-        };
-        auto take_finite = [&](const uint4& v) {
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t lo = u[e] & 0x7FFFu, hi = (u[e] >> 16) & 0x7FFFu;
-                amax = lo < 0x7F80u && lo > amax ? lo : amax;
-                amax = hi < 0x7F80u && hi > amax ? hi : amax;
-            }
-        };
-        auto row = [&](int r) { return __ldg(reinterpret_cast<const uint4*>(x + (t + r) * stride)); };
         // the largest over the lanes of the run's warps
         auto over_unit = [&](uint32_t v) {
             v = __reduce_max_sync(0xffffffffu, v);
@@ -176,6 +165,31 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) append_paged_fp8_kerne
             }
             return v;
         };
+        uint32_t amax = 0;  // the largest magnitude, as two bf16; 0x7F80 and above: not a finite number
+        auto take = [&](const uint4& v) {
+            amax = __vmaxu2(amax, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                           __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+        };
+        auto row = [&](int r) { return __ldg(reinterpret_cast<const uint4*>(x + static_cast<long long>(t + r) * stride)); };
+        auto take_finite = [&](const uint4& v) {
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t lo = u[e] & 0x7FFFu, hi = (u[e] >> 16) & 0x7FFFu;
+                amax = lo < 0x7F80u && lo > amax ? lo : amax;
+                amax = hi < 0x7F80u && hi > amax ? hi : amax;
+            }
+        };
+        // rows that will not stay in registers come first, as many at once
+#pragma unroll 1
+        for (int r = r0 + HOLD * rstep; r < n; r += HOLD * rstep) {
+#pragma unroll
+            for (int i = 0; i < HOLD; ++i) {
+                hold[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (r + i * rstep < n) hold[i] = row(r + i * rstep);
+            }
+#pragma unroll
+            for (int i = 0; i < HOLD; ++i) take(hold[i]);
+        }
 #pragma unroll
         for (int i = 0; i < HOLD; ++i) {
             hold[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -185,7 +199,6 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) append_paged_fp8_kerne
         const float s_old = first > 0 ? scales[page * p.H] : 0.f;
 #pragma unroll
         for (int i = 0; i < HOLD; ++i) take(hold[i]);
-        for (int r = r0 + HOLD * rstep; r < n; r += rstep) take(row(r));
         amax = over_unit((amax >> 16) > (amax & 0xFFFFu) ? amax >> 16 : amax & 0xFFFFu);
         const bool all = amax >= 0x7F80u;  // infinities or NaN among the rows: the largest finite one
         if (all) {
@@ -211,11 +224,18 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) append_paged_fp8_kerne
         if (dense) {
             uint8_t* at = page_rows + (first + r0) * row_bytes;
             const long long step = rstep * row_bytes;
+#pragma unroll 1
+            for (int r = r0;;) {
 #pragma unroll
-            for (int i = 0; i < HOLD; ++i)
-                if (r0 + i * rstep < n) store(at + i * step, hold[i]);
-            at += HOLD * step;
-            for (int r = r0 + HOLD * rstep; r < n; r += rstep, at += step) store(at, row(r));
+                for (int i = 0; i < HOLD; ++i)
+                    if (r + i * rstep < n) store(at + i * step, hold[i]);
+                r += HOLD * rstep;
+                if (r >= n) break;
+                at += HOLD * step;
+#pragma unroll
+                for (int i = 0; i < HOLD; ++i)
+                    if (r + i * rstep < n) hold[i] = row(r + i * rstep);
+            }
         } else {
             for (int r = r0; r < n; r += rstep) {
                 // a slot named again by a later token of the run keeps that token's row
@@ -227,7 +247,7 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) append_paged_fp8_kerne
         }
     };
 
-    for (long long t32 = t_lo; t32 < t_hi; t32 += 32) {
+    for (unsigned int t32 = t_lo; t32 < t_hi; t32 += 32) {
         // the tokens of these 32 that start a run (the same in every warp)
         bool start = false;
         long long slot = -1;
