@@ -13,15 +13,16 @@
 // lie in one page; of every run and head the work is: the largest finite |x| of
 // the new rows, the scale, the old rows if the scale grew, the new rows.  A CTA
 // takes `chunk` tokens of one head of K or V and the runs that start there.
-// It has a warp for every 16 rows of a page (1 to 8): where its runs are long
+// It has a warp for every 16 rows of a page (1 to 4): where its runs are long
 // they share the rows of one run after the other, where there are as many runs
 // as warps (decode steps) each warp takes runs of its own.  The first 16 rows of
 // a warp (d = 128) stay in registers between the two passes, the rest comes
 // again from L2, 16 rows in flight at once.  17.8k tokens of 8 heads of 128 take
-// 22, 23, 26, 30 and 30 us in pages of 16, 32, 64, 128 and 256 (16.7 for the
+// 22, 23, 26, 26 and 31 us in pages of 16, 32, 64, 128 and 256 (16.7 for the
 // bytes alone): what is left is the chain of a run, slots -> rows -> maximum ->
-// codes, and 62 % of the issue slots.  chunk grows from 1 (a decode step, too few tokens to fill the
-// GPU) to a page (a prefill, where most tokens start no run).
+// codes, and 62 % of the issue slots.  chunk grows from 1 (a decode step, too
+// few tokens to fill the GPU) to a page (a prefill, where most tokens start no
+// run).
 #pragma once
 
 #include <cuda_bf16.h>
