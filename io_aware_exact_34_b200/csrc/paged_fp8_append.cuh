@@ -20,7 +20,7 @@
 // again from L2, 16 rows in flight at once.  17.8k tokens of 8 heads of 128 take
 // 22, 23, 26, 26 and 31 us in pages of 16, 32, 64, 128 and 256 (16.7 for the
 // bytes alone): what is left is the chain of a run, slots -> rows -> maximum ->
-// codes, and 62 % of the issue slots.  chunk grows from 1 (a decode step, too
+// codes, and 60 % of the issue slots.  chunk grows from 1 (a decode step, too
 // few tokens to fill the GPU) to a page (a prefill, where most tokens start no
 // run).
 #pragma once
