@@ -112,6 +112,21 @@ def test_fwd_argument_checks(fl):
     assert _attend(fl, "fwd", B=1, T=3, most=3, width=256, bytes=need - 1) == fl.FATTN_ERR_WORKSPACE
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_more_keys_never_mean_fewer_splits(fl, d):
+    """A workspace sized for the whole table serves every window of it."""
+    lens = sorted({1 << e for e in range(25)} | {(1 << e) + 1 for e in range(4, 24)} | set(range(100, 40000, 997)))
+    for B in (1, 2, 5, 8, 16, 24, 33, 64, 100, 200, 512, 3000):
+        for Hq, Hkv in ((8, 8), (32, 8), (16, 1), (71, 1), (10, 2)):
+            splits = [fl.attn_decode_paged_fp8_auto_splits(B, Hq, Hkv, n, d) for n in lens]
+            assert all(x <= y for x, y in zip(splits, splits[1:])), (B, Hq, Hkv, splits)
+            assert all(1 <= x <= 64 and x <= -(-n // 256) for x, n in zip(splits, lens))
+            for new in (2, 3, 8):
+                if new * (Hq // Hkv) < 49:
+                    need = [fl.attn_fwd_paged_fp8_workspace_bytes(B, B * new, new, Hq, Hkv, n, d) for n in lens]
+                    assert all(x <= y for x, y in zip(need, need[1:])), (B, Hq, Hkv, new, need)
+
+
 def test_reference_rounding():
     """The reference's e4m3 against torch's conversion, on every value and every midpoint."""
     v = ref.TABLE[:127]
