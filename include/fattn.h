@@ -417,6 +417,7 @@ int attn_append_paged_fp8(const void* k, const void* v, long long k_stride, long
  *   num_splits   splits of a sequence's attended keys at most (evenly, by the
  *                sequence's own length, at least 256 keys to a split), or 0 for
  *                attn_decode_paged_fp8_auto_splits(B, Hq, Hkv, max_pages*page_size, d)
+ *                (with a window of fewer keys: as many as for those keys, never more)
  *   workspace    device scratch of attn_decode_workspace_bytes(B, Hq, Lk, d, S)
  *                bytes for S splits, 16-byte aligned; not needed (may be NULL)
  *                when S = 1; contents ignored on entry, unspecified on return
