@@ -101,6 +101,24 @@ def test_plan_saturates(fl):
     assert table.tolist() == [[0, 1]] * 3
 
 
+def test_plan_results_stand_alone(fl):
+    """The results of one call can be changed, kept and fed back one by one."""
+    for B in (1, 31, 32, 33, 500):
+        table = _i32([[b] for b in range(B)])
+        got = fl.attn_paged_plan(_i32([1] * B), _i32([2] * B), _i32([]), table, 16, 2 * B)
+        want = [t.tolist() for t in got]
+        assert want[1] == list(range(0, 2 * B + 1, 2)) and want[2] == [3] * B and want[3] == [2 * B, 0]
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in got)
+        assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
+        assert all(t.is_contiguous() and t.data_ptr() % 128 == 0 for t in got)
+        for i, t in enumerate(got):
+            t.fill_(-9)
+            assert [x.tolist() for x in got[i + 1:]] == want[i + 1:]
+        got = fl.attn_paged_plan(_i32([1] * B), _i32([2] * B), _i32([]), table, 16, 2 * B)
+        again = fl.attn_paged_plan(got[2], _i32([1] * B), _i32([]), table, 16, B)
+        assert again[2].tolist() == [4] * B and got[2].tolist() == [3] * B
+
+
 # ---------------------------------------------------------------- append
 def _append_and_check(fl, x, slots, cache, page):
     """x: bf16 (k, v) on the GPU, any token stride; cache: CPU codes and scales."""
