@@ -859,7 +859,7 @@ __global__ void __launch_bounds__(256) merge_ext_kernel(const __grid_constant__ 
     for (int e = 0; e < 2; ++e) {
         const int r = (blockIdx.x & 15) * 16 + e * 8 + (threadIdx.x >> 5);
         if (r < rows)
-            merge_row<D>(p.c, static_cast<long long>(it.q0) + it.tok[0] + r / p.c.g, h * p.c.g + r % p.c.g, it.active, p.splits);
+            merge_row<D, false>(p.c, static_cast<long long>(it.q0) + it.tok[0] + r / p.c.g, h * p.c.g + r % p.c.g, it.active, p.splits);
     }
 }
 

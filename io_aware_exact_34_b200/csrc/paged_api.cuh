@@ -174,8 +174,11 @@ int launch_dp8(PagedFp8Params p, int d, int num_splits, void* workspace, size_t 
     }
     if (st != FATTN_OK || p.S == 1 || p.cluster) return st;
     const long long merge_grid = (static_cast<long long>(p.B) * p.max_q * p.Hq + 3) / 4;  // a warp per row
-    return d == 128 ? launch_merge(merge_paged_fp8_kernel<128>, merge_grid, 128, s, p, tile_rows)
-                    : launch_merge(merge_paged_fp8_kernel<64>, merge_grid, 128, s, p, tile_rows);
+    if (p.S > 64)
+        return d == 128 ? launch_merge(merge_paged_fp8_kernel<128, true>, merge_grid, 128, s, p, tile_rows)
+                        : launch_merge(merge_paged_fp8_kernel<64, true>, merge_grid, 128, s, p, tile_rows);
+    return d == 128 ? launch_merge(merge_paged_fp8_kernel<128, false>, merge_grid, 128, s, p, tile_rows)
+                    : launch_merge(merge_paged_fp8_kernel<64, false>, merge_grid, 128, s, p, tile_rows);
 }
 
 // Rows (new tokens x group heads) of a sequence from which its tiles go to the

@@ -279,6 +279,14 @@ def test_decode_matches_reference(fl, lens, page, hq, hkv, d, left, splits):
     _decode_case(fl, lens, page, hq, hkv, d, seed=sum(lens) + hq, left=left, splits=splits)
 
 
+@pytest.mark.parametrize("splits,left", [(65, -1), (100, -1), (128, -1), (128, 20000), (200, -1)])
+def test_decode_more_than_64_splits(fl, splits, left):
+    """As many parts of a sequence as num_splits asks for, beside sequences that have fewer of them."""
+    lens = [33280, 700, 24001, 0, 16640]
+    _decode_case(fl, lens, 16, 4, 2, 128, seed=splits, left=left, splits=splits, q_gain=8.0)
+    _decode_case(fl, lens, 64, 3, 1, 64, seed=splits + 1, left=left, splits=splits, q_gain=8.0)
+
+
 @pytest.mark.parametrize("spread,q_gain", [(20, 1.0), (5, 30.0), (0, 1e-20), (2, 0.0)])
 def test_decode_ranges(fl, spread, q_gain):
     """Page scales far apart, sharp and flat softmax rows."""
