@@ -650,7 +650,11 @@ __global__ void __launch_bounds__(384, 1)
             }
             if (pending) {
                 const bool part = active > 1;  // a part writes its (o, lse) to the workspace
-                const long long ws_row = q_row * p.splits + split;
+                long long ws_row = 0;  // its place in the workspace, which has the rows of the cut pairs alone
+                if (part) {
+                    const int cut = static_cast<int>(static_cast<unsigned>(item - p.n_whole) / static_cast<unsigned>(p.splits));
+                    ws_row = static_cast<long long>((cut * 2 + t) * p.toks * p.c.g + row) * p.splits + split;
+                }
                 float* lse = nullptr;
                 if (p.c.lse != nullptr) lse = p.c.lse + q_row / p.c.Hq * p.c.lse_tok + q_row % p.c.Hq * p.c.lse_head;
                 if (!visited) {
@@ -850,7 +854,7 @@ __global__ void __launch_bounds__(384, 1)
 template <int D>
 __global__ void __launch_bounds__(256) merge_ext_kernel(const __grid_constant__ ExtParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int pb = p.n_whole + (blockIdx.x >> 4);
+    const int cut = blockIdx.x >> 4, pb = p.n_whole + cut;
     const int bh = pb / p.n_pairs, h = bh % p.c.Hkv;
     const ExtItem it = ext_pair(p, bh / p.c.Hkv, h, p.n_pairs - 1 - pb % p.n_pairs, 0, p.splits);
     if (it.active <= 1) return;
@@ -859,7 +863,8 @@ __global__ void __launch_bounds__(256) merge_ext_kernel(const __grid_constant__ 
     for (int e = 0; e < 2; ++e) {
         const int r = (blockIdx.x & 15) * 16 + e * 8 + (threadIdx.x >> 5);
         if (r < rows)
-            merge_row<D, false>(p.c, static_cast<long long>(it.q0) + it.tok[0] + r / p.c.g, h * p.c.g + r % p.c.g, it.active, p.splits);
+            merge_row<D, false>(p.c, static_cast<long long>(it.q0) + it.tok[0] + r / p.c.g, h * p.c.g + r % p.c.g,
+                                static_cast<long long>(cut) * 2 * p.toks * p.c.g + r, it.active, p.splits);
     }
 }
 

@@ -81,7 +81,7 @@ struct PagedFp8Params {
     const int* cu_q;            // [B + 1], or null: one token per sequence, token b
     __nv_bfloat16* o;
     float* lse;                 // or null
-    float *ws_o, *ws_lse;       // partials [row][split][d], [row][split]
+    float *ws_o, *ws_lse;       // partials [row][split][d], [row][split]; rows of the output, or of the pairs that are cut
     long long lse_tok, lse_head;  // strides of lse
     int B, Hq, Hkv, g, total_q, max_q;
     int max_pages, page_shift, num_pages;
@@ -721,14 +721,14 @@ __global__ void __launch_bounds__(32 * DP8_WARPS, dp8_resident(D, 8 * NT, kMaske
     cluster_sync();  // nobody leaves while its part may still be read
 }
 
-// One warp: the row of packed token tok and query head hq from its `active` partial (o, lse) pairs, `stride` of them to a row in the
-// workspace.  kMany: more than 64 of them may be active (for one variant of both, 16 x 5 drafted tokens take 23.8 us instead of 23.4).
+// One warp: the row of packed token tok and query head hq from its `active` partial (o, lse) pairs, those of the workspace's row
+// ws_row, which has room for `stride` of them.  kMany: more than 64 of them may be active (for one variant of both, 16 x 5 drafted tokens take 23.8 us instead of 23.4).
 template <int D, bool kMany>
-__device__ __forceinline__ void merge_row(const PagedFp8Params& p, long long tok, int hq, int active, int stride) {
+__device__ __forceinline__ void merge_row(const PagedFp8Params& p, long long tok, int hq, long long ws_row, int active, int stride) {
     constexpr int EPL = D / 32;  // elements per lane
     const int lane = threadIdx.x & 31;
     const long long r = tok * p.Hq + hq;
-    const float* ls = p.ws_lse + r * stride;
+    const float* ls = p.ws_lse + ws_row * stride;
     // lane s holds the lse of parts s and s + 32
     const float x0 = lane < active ? ls[lane] : -CUDART_INF_F, x1 = lane + 32 < active ? ls[lane + 32] : -CUDART_INF_F;
     float M = fmaxf(x0, x1);
@@ -747,7 +747,7 @@ __device__ __forceinline__ void merge_row(const PagedFp8Params& p, long long tok
     float W = 0.f, f[EPL];
 #pragma unroll
     for (int e = 0; e < EPL; ++e) f[e] = 0.f;
-    const float* src = p.ws_o + r * stride * D + lane * EPL;
+    const float* src = p.ws_o + ws_row * stride * D + lane * EPL;
     auto add = [&](float wt, bool some) {
         W += wt;
         // a part without a key of this row may not have written its o
@@ -794,7 +794,8 @@ __global__ void __launch_bounds__(128) merge_paged_fp8_kernel(const PagedFp8Para
     const int row0 = row / tile_rows * tile_rows;
     const int rows = n_tok * p.g - row0 < tile_rows ? n_tok * p.g - row0 : tile_rows;
     const SplitSpan sp = split_span(p, sq, row0 / p.g, (row0 + rows - 1) / p.g, 0);
-    if (sp.active > 1) merge_row<D, kMany>(p, static_cast<long long>(sq.q0) + i, hq, sp.active, p.S);  // else written by the split kernel
+    const long long tok = static_cast<long long>(sq.q0) + i;
+    if (sp.active > 1) merge_row<D, kMany>(p, tok, hq, tok * p.Hq + hq, sp.active, p.S);  // else written by the split kernel
 }
 
 }  // namespace fattn

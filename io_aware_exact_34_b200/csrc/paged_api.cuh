@@ -218,9 +218,12 @@ int ext_splits(long long pairs, long long tiles, int toks, int g, int d) {
     return best;
 }
 
-// The item counter, then the parts' (o, lse).
+// Rows of the pairs that are cut into parts: those of the last, incomplete round.
+long long ext_cut_rows(long long pairs, int g) { return pairs % kSms * 2 * (128 / g) * g; }
+
+// The item counter, then the parts' (o, lse) of those rows (2048 tokens of 32 heads over 131072 keys: 57 MB).
 constexpr size_t kExtCounterBytes = 32;
-size_t ext_workspace(long long rows, int S, int d) { return kExtCounterBytes + parts_bytes(rows, S, d); }
+size_t ext_workspace(long long pairs, int S, int g, int d) { return kExtCounterBytes + parts_bytes(ext_cut_rows(pairs, g), S, d); }
 
 // The pool [num_pages * page_size, Hkv, d] of codes: boxes of box_rows keys of one head.
 int encode_map_pages(CUtensorMap* map, const void* base, int d, int Hkv, long long rows, int box_rows) {
@@ -240,7 +243,6 @@ int launch_ext(const PagedFp8Params& c, int d, long long pool_rows, void* worksp
     p.toks = 128 / c.g;
     p.n_pairs = static_cast<int>(ext_pairs(c.max_q, c.g));
     const long long pairs = static_cast<long long>(c.B) * c.Hkv * p.n_pairs;
-    const long long rows = static_cast<long long>(c.total_q) * c.Hq;
     const long long all_tiles = ((static_cast<long long>(c.max_pages) << c.page_shift) + 127) / 128;
     p.splits = ext_splits(pairs, all_tiles, p.toks, c.g, d);  // what the workspace is sized for
     if (c.window_left >= 0 && (c.causal || c.window_right >= 0)) {
@@ -252,11 +254,11 @@ int launch_ext(const PagedFp8Params& c, int d, long long pool_rows, void* worksp
     p.n_whole = static_cast<int>(p.splits == 1 ? pairs : pairs - pairs % kSms);
     const long long cut = pairs - p.n_whole, n_items = p.n_whole + cut * p.splits;
     if (pairs > 0x07ffffffLL) return FATTN_ERR_UNSUPPORTED;
-    if (!workspace || workspace_bytes < ext_workspace(rows, p.splits, d)) return FATTN_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < ext_workspace(pairs, p.splits, c.g, d)) return FATTN_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 31u) return FATTN_ERR_MISALIGNED;
     p.counter = static_cast<unsigned int*>(workspace);
     p.c.ws_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + kExtCounterBytes);
-    p.c.ws_lse = p.c.ws_o + rows * p.splits * d;
+    p.c.ws_lse = p.c.ws_o + ext_cut_rows(pairs, c.g) * p.splits * d;
     p.n_items = static_cast<int>(n_items);
     const int page_size = 1 << c.page_shift;
     p.box_rows = page_size < 128 ? page_size : 128;
@@ -412,8 +414,10 @@ size_t attn_fwd_paged_fp8_workspace_bytes(int B, int total_q, int max_seqlen_q, 
     const long long max_q = max_seqlen_q < total_q ? max_seqlen_q : total_q;
     const int g = Hq / Hkv;
     const long long rows = max_q * g, all = static_cast<long long>(total_q) * Hq;
-    if (g <= 128 && ext_path(max_q, g))
-        return ext_workspace(all, ext_splits(static_cast<long long>(B) * Hkv * ext_pairs(max_q, g), (static_cast<long long>(Lk) + 127) / 128, 128 / g, g, d), d);
+    if (g <= 128 && ext_path(max_q, g)) {
+        const long long pairs = static_cast<long long>(B) * Hkv * ext_pairs(max_q, g);
+        return ext_workspace(pairs, ext_splits(pairs, (static_cast<long long>(Lk) + 127) / 128, 128 / g, g, d), g, d);
+    }
     const int t = dp8_tile_rows(rows, max_q > 1);
     return parts_bytes(all, dp8_auto_splits(static_cast<long long>(B) * Hkv * ((rows + t - 1) / t), Lk, d, t, max_q > 1), d);
 }

@@ -471,6 +471,38 @@ def test_fwd_nan_values_in_parts(fl):
     _fwd_case(fl, [2900], [90], 32, 4, 1, 64, seed=6, left=1500, nan_v=[(0, 2895, 0, 5), (0, 1330, 0, 0), (0, 1400, 0, 63)])
 
 
+@pytest.mark.parametrize("lens,new,page,hq,hkv,d,left", [
+    ([5000, 900], [1300, 60], 64, 32, 8, 128, -1), ([3000], [2500], 16, 16, 16, 64, -1), ([3000], [2500], 16, 16, 16, 64, 700),
+    ([4000], [401], 128, 71, 1, 128, -1), ([16000, 40], [600, 3], 256, 8, 8, 128, -1),
+])
+def test_fwd_whole_and_cut_pairs(fl, lens, new, page, hq, hkv, d, left):
+    """More pairs of row tiles than one round holds, the last round's cut into parts, in a workspace of the size asked for
+    and no byte more: rows of both kinds, and the same bits as with the library's own workspace."""
+    g = torch.Generator().manual_seed(sum(new) + hq)
+    width = -(-max(lens) // page) + 1
+    pages = sum(-(-x // page) for x in lens) + 1
+    table = _table(lens, page, width, pages, g)
+    cache = _cache(pages, page, hkv, d, g)
+    q = torch.randn(sum(new), hq, d, generator=g).to(torch.bfloat16)
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    args = (q.cuda(), *[t.cuda() for t in cache], _i32(table), _i32(lens), _i32(cu), max(new))
+    need = fl.attn_fwd_paged_fp8_workspace_bytes(len(lens), sum(new), max(new), hq, hkv, width * page, d)
+    buf = torch.full((need + 128,), 0x5A, dtype=torch.uint8, device="cuda")
+    o, lse = fl.attn_fwd_paged_fp8(*args, causal=True, window_left=left, workspace=buf[64:64 + need])
+    assert bool((buf[:64] == 0x5A).all()) and bool((buf[64 + need:] == 0x5A).all())
+    o2, lse2 = fl.attn_fwd_paged_fp8(*args, causal=True, window_left=left)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    kv, vv = ref.value(cache[0]), ref.value(cache[1])
+    for b, n in enumerate(new):
+        k, v = ref.gather(kv, cache[2].double(), table[b], lens[b]), ref.gather(vv, cache[3].double(), table[b], lens[b])
+        for i in sorted({0, 1, n - 1, n // 2} | set(torch.randint(0, n, (12,), generator=g).tolist())):
+            at, seen = cu[b] + i, lens[b] - n + i + 1
+            exp = ref.attention(q[at][None].double(), k[:seen], v[:seen], float(torch.tensor(d ** -0.5, dtype=torch.float32)), left=left)
+            _check_rows(o[at][None], lse[:, at][None], exp, d, seen, f"sequence {b}, token {i}")
+
+
 def test_fwd_one_token_is_decode(fl):
     """One new token per sequence: the rows of attn_decode_paged_fp8, bit for bit when both choose the same splits."""
     g = torch.Generator().manual_seed(21)

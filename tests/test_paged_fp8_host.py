@@ -127,6 +127,27 @@ def test_more_keys_never_mean_fewer_splits(fl, d):
                     assert all(x <= y for x, y in zip(need, need[1:])), (B, Hq, Hkv, new, need)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_long_run_workspace_holds_the_cut_pairs(fl, d):
+    """Only the pairs of row tiles of the last, incomplete round of 148 are cut into (at most 32) parts: the workspace of
+    a long run has their rows and no others."""
+    for B in (1, 2, 3, 5, 16, 64, 300):
+        for new in (49, 300, 1984, 2048, 4800, 8192, 30000):
+            for Hq, Hkv in ((32, 8), (8, 8), (128, 8), (71, 1), (16, 1), (5, 1), (128, 1)):
+                g = Hq // Hkv
+                toks = 128 // g
+                pairs = B * Hkv * -(--(-new // toks) // 2)
+                for Lk in (64, 4096, 32768, 131072, 1 << 20):
+                    need = fl.attn_fwd_paged_fp8_workspace_bytes(B, B * new, new, Hq, Hkv, Lk, d)
+                    rows = pairs % 148 * 2 * toks * g
+                    assert 32 <= need <= 32 + rows * 32 * (d + 1) * 4, (B, new, Hq, Hkv, Lk)
+                    assert rows == 0 or (need - 32) % (rows * (d + 1) * 4) == 0
+    # as a caller meets it: what was 1.4, 2.2, 3.1, 3.8 and 52 GB by all rows
+    for B, new, Hq, Lk, most in ((1, 4800, 32, 131072, 20), (16, 2048, 32, 32768, 56), (3, 1984, 32, 32768, 18), (4, 8192, 32, 131072, 89),
+                                 (3, 8192, 128, 131072, 18)):
+        assert fl.attn_fwd_paged_fp8_workspace_bytes(B, B * new, new, Hq, 8, Lk, 128) <= most << 20
+
+
 def test_reference_rounding():
     """The reference's e4m3 against torch's conversion, on every value and every midpoint."""
     v = ref.TABLE[:127]
