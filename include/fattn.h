@@ -423,10 +423,15 @@ int attn_append_paged_fp8(const void* k, const void* v, long long k_stride, long
  *                when S = 1; contents ignored on entry, unspecified on return
  * Codes enter the products exactly (as f16), a query row is scaled by a power of
  * two before it is rounded to f16 (exact down to 2^-14 of the row's largest
- * element), probabilities are rounded to f16 (2^-11 of each), sums and
- * statistics are fp32, O is rounded to bf16 once.  Key rows outside the attended
- * range have no effect, whatever their codes are (NaN included).  The V scales
- * of one sequence may differ by up to 2^80; one below 2^-80 counts as 2^-80.
+ * element), sums and statistics are fp32, O is rounded to bf16 once.  A
+ * probability enters the product with V as f16, together with its page's V scale:
+ * p * vs is rounded by 2^-11 of itself down to 2^-21 of the row's largest p * vs,
+ * and by up to 2^-32 of that largest below.  So a page whose V scale is far below
+ * another's keeps all bits up to 2^21 * (its p / the other's p), then fewer, and
+ * from 2^32 on its values are lost - also where the other page's codes are 0.  LSE
+ * and the probabilities' sum hold for V scales up to 2^80 apart; one below
+ * 2^-80 counts as 2^-80.  Key rows outside the attended range have no effect,
+ * whatever their codes are (NaN included).
  */
 int attn_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
                           const float* k_scales, const float* v_scales,

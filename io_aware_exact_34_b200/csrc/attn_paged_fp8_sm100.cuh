@@ -15,8 +15,9 @@
 //   both go through the same accumulator: 2 x 4 products of 32 elements, the
 //   time of one bf16 product, with no conversion of K.  The split is exact down
 //   to 2^-10 of the row's largest element, and off by at most 2^-18 of it below.
-//   O += P V runs on f16 (kind::f16): P keeps 11 bits and a range of 2^-31 below
-//   the reference (e4m3 would lose long tails), V's codes convert exactly.  Two
+//   O += P V runs on f16 (kind::f16): p * vs keeps 11 bits down to 2^-21 of the
+//   row's largest and is off by up to 2^-32 of it below (e4m3 would lose long
+//   tails), V's codes convert exactly.  Two
 //   warps convert each V tile once for both row tiles, from its 8-bit stage into
 //   an f16 tile in the 128-byte-swizzled layout the tensor core reads.
 //

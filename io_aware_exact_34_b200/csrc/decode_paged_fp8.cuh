@@ -10,15 +10,17 @@
 // running reference my follows y, not x: p' = 2^(y - my + 7) <= 2^15 goes into
 // the P V product as f16, l sums p' / vs in fp32, and o = acc / l,
 // lse = my + log2 l - 7.  So one exponential serves both sums, and the largest
-// term of the numerator always sits in f16's normal range, whatever the pages'
-// scales are.  The reference moves only when some y passes it by more than 8
-// (as in the prefill kernels), which keeps reductions out of the loop.
+// p * vs of the numerator always sits in f16's normal range, whatever the pages'
+// scales are.  A smaller one is rounded by 2^-11 of itself down to p' = 2^-14, 2^-21
+// of the largest, and by half a subnormal step below, 2^-25: 2^-32 of the largest.
+// The reference moves only when some y passes it by more than 8 (as in the
+// prefill kernels), which keeps reductions out of the loop.
 //
 // Products run on mma.sync m16n8k16 with f16 operands and fp32 accumulation:
 // e4m3 is a subset of f16, so codes convert exactly; a query row is scaled by
 // a power of two to a largest magnitude in [1, 2) before it becomes f16 (11
 // bits against bf16's 8, so nothing is lost down to 2^-14 of the row's
-// largest element); P is rounded to f16 (relative 2^-11).  The key rows are the
+// largest element); P is rounded to f16 (see above).  The key rows are the
 // M operand and 8 query rows the N operand: S^T = K Q^T and O^T = V^T P^T waste
 // nothing at 8 rows a group, where Q as the M operand would pay for 16.
 // (mma.sync on e4m3 operands, with Q as two e4m3 terms, was measured: it is

@@ -549,6 +549,43 @@ def test_value_scale_of_nothing(fl):
             assert bool(((lse.double().cpu() - exp[1]).abs() <= ref.tolerances(*[exp[i] for i in (0, 2, 3)], 128, 60)[1]).all())
 
 
+@pytest.mark.parametrize("new", [1, 4, 60])
+@pytest.mark.parametrize("d,hq,hkv", [(128, 4, 2), (64, 3, 1)])
+def test_value_scales_far_apart(fl, new, d, hq, hkv):
+    """Pages with a V scale 2^ratio times that of the others and nothing but zero codes: O is the others' rows alone.
+
+    P is rounded as f16 of p' = 2^7 p vs / m, with m at most the row's largest p vs: by 2^-11 of itself, or by half a
+    subnormal step, 2^-25, which is 2^-32 m in p vs.  So beside the other roundings O is off by up to 2^-32 m sum |code|."""
+    g = torch.Generator().manual_seed(25)
+    pages, page = 12, 16
+    L, scale = pages * page - 3, float(torch.tensor(d ** -0.5, dtype=torch.float32))
+    kc, vc, ks, _ = _cache(pages, page, hkv, d, g)
+    vc[[0, 5]] = 0
+    q = torch.randn(new, hq, d, generator=g).to(torch.bfloat16)
+    k = ref.gather(ref.value(kc), ks.double(), list(range(pages)), L)
+    codes = ref.value(vc).reshape(-1, hkv, d)[:L]
+    for ratio in (0, 12, 20, 24, 28, 32, 40, 80):
+        vs = torch.full((pages, hkv), 2.0 ** -12)
+        vs[[0, 5]] = 2.0 ** (ratio - 12)
+        v = ref.gather(ref.value(vc), vs.double(), list(range(pages)), L)
+        if new == 1:
+            o, lse = fl.attn_decode_paged_fp8(q[:, :, None].cuda(), kc.cuda(), vc.cuda(), ks.cuda(), vs.cuda(), _i32([list(range(pages))]), _i32([L]))
+            o = o[:, :, 0]
+        else:
+            o, lse = fl.attn_fwd_paged_fp8(q.cuda(), kc.cuda(), vc.cuda(), ks.cuda(), vs.cuda(), _i32([list(range(pages))]), _i32([L]), _i32([0, new]), new)
+            lse = lse.T
+        eo, el, w, dots = ref.attention(q.double(), k, v, scale, causal=False)
+        to, tl = ref.tolerances(eo, w, dots, d, L)
+        for j in range(hq):
+            p = torch.softmax(q[:, j].double() @ k[:, j // (hq // hkv)].T * scale, -1)
+            most = (p * vs.double()[torch.arange(L) // page, j // (hq // hkv)]).amax(-1)
+            to[:, j] += 1.01 * 2.0 ** -32 * most[:, None] * codes[:, j // (hq // hkv)].abs().sum(0)
+        assert bool(((o.double().cpu() - eo).abs() <= to).all()), ratio
+        assert bool(((lse.double().cpu() - el).abs() <= tl).all()), ratio
+        if ratio <= 20:  # above 2^-21 m the other pages' p vs keep their bits: O is off by its own rounding and theirs
+            assert float((o.double().cpu() - eo).norm() / eo.norm()) < 2.0 ** -8, ratio
+
+
 def test_buffers_given(fl):
     """Outputs and workspaces of the caller's: the same results as with the library's choice."""
     g = torch.Generator().manual_seed(24)
