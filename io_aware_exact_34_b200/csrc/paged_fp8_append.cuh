@@ -239,10 +239,11 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) append_paged_fp8_kerne
             }
         } else {
             for (int r = r0; r < n; r += rstep) {
-                // a slot named again by a later token of the run keeps that token's row
+                // a slot named again by a later token of the run keeps that token's row; looking only as far as the
+                // next such token, all looks of a slot together pass the run once: n * page_size steps at most, not n * n
                 const long long slot = __ldg(p.slots + t + r);
                 bool again = false;
-                for (int i = r + 1; i < n; ++i) again |= __ldg(p.slots + t + i) == slot;
+                for (int i = r + 1; i < n && !again; ++i) again = __ldg(p.slots + t + i) == slot;
                 if (!again) store(page_rows + (slot & page_mask) * row_bytes, row(r));
             }
         }

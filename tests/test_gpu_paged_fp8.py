@@ -162,6 +162,26 @@ def test_append_skips_and_duplicates(fl):
     _append_and_check(fl, (x[:, 0], x[:, 1]), slots, cache, 16)
 
 
+@pytest.mark.parametrize("slots", [[20], [20, 21], [16, 17, 17, 18, 31]])
+def test_append_many_tokens_of_few_slots(fl, slots):
+    """A long stretch over a few slots (a batch padded with one spare slot) takes time linear in its tokens."""
+    g = torch.Generator().manual_seed(6)
+    cache = _cache(3, 16, 1, 64, g)
+    n = 60000
+    slots = sorted(slots * (n // len(slots))) if len(slots) > 2 else slots * (n // len(slots))
+    x = torch.randn(len(slots), 2, 1, 64, generator=g).to(torch.bfloat16).cuda()
+    _append_and_check(fl, (x[:, 0], x[:, 1]), slots, cache, 16)
+    dev = [t.cuda() for t in cache]
+    at = torch.tensor(slots, dtype=torch.int64, device="cuda")
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    begin.record()
+    fl.attn_append_paged_fp8(x[:, 0], x[:, 1], at, *dev)
+    end.record()
+    torch.cuda.synchronize()
+    # n / 4 rows a lane at a few loads each; a look through the whole rest of the stretch for each would be 4e8 loads a lane
+    assert begin.elapsed_time(end) < 500.0
+
+
 def test_append_extremes(fl):
     """Zeros, subnormals, the largest bf16, exact scale borders, infinities and NaN."""
     g = torch.Generator().manual_seed(2)
