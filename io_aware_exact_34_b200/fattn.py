@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import importlib.util
+import operator
 import os
 
 import torch
@@ -431,6 +432,19 @@ def _first(t, dtype, ndim, name):
 _stream_of = torch._C._cuda_getCurrentRawStream  # device index -> cudaStream_t
 
 
+def _int32(x, name):
+    """An integer that the C ABI takes in 32 bits: ctypes would drop its upper ones."""
+    x = operator.index(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name}: {x} is beyond 32 bits")
+    return x
+
+
+def _window(x):
+    """A window's length for the C ABI: negative is unlimited, and 2^31 - 1 is wider than any sequence."""
+    return max(-1, min(operator.index(x), 2 ** 31 - 1))
+
+
 def attn_paged_plan(seqlens_k, seqlens_new, free_pages, block_table, page_size, max_tokens, slot_map=None,
                     cu_seqlens=None, seqlens_out=None, counts=None):
     """Where the new tokens of a batch go in a paged cache.  seqlens_k,
@@ -444,6 +458,7 @@ def attn_paged_plan(seqlens_k, seqlens_new, free_pages, block_table, page_size, 
         got = _calls.plan(seqlens_k, seqlens_new, free_pages, block_table, page_size, max_tokens)
         if got is not None:
             return got
+    page_size, max_tokens = _int32(page_size, "page_size"), _int32(max_tokens, "max_tokens")
     dev = _first(seqlens_k, _I32, 1, "seqlens_k")
     B = seqlens_k.shape[0]
     _need(seqlens_new, _I32, (B,), dev, "seqlens_new")
@@ -528,7 +543,7 @@ def attn_append_paged_fp8(k, v, slot_map, k_pages, v_pages, k_scales, v_scales):
 
 
 def attn_decode_paged_fp8_auto_splits(B, Hq, Hkv, Lk, d) -> int:
-    return lib.attn_decode_paged_fp8_auto_splits(B, Hq, Hkv, Lk, d)
+    return lib.attn_decode_paged_fp8_auto_splits(B, Hq, Hkv, _int32(Lk, "Lk"), d)
 
 
 def _want_heads(Hq, d, Hkv, dk):
@@ -545,6 +560,7 @@ def attn_decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, 
         got = _calls.decode(q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, scale, window_left, num_splits)
         if got is not None:
             return got
+    window_left, num_splits = _window(window_left), _int32(num_splits, "num_splits")
     dev = _first(q, _BF16, 4, "q")
     B, Hq, Lq, d = q.shape
     if Lq != 1:
@@ -579,7 +595,8 @@ def attn_decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, 
 
 
 def attn_fwd_paged_fp8_workspace_bytes(B, total_q, max_seqlen_q, Hq, Hkv, Lk, d) -> int:
-    return lib.attn_fwd_paged_fp8_workspace_bytes(B, total_q, max_seqlen_q, Hq, Hkv, Lk, d)
+    return lib.attn_fwd_paged_fp8_workspace_bytes(B, _int32(total_q, "total_q"), _int32(max_seqlen_q, "max_seqlen_q"), Hq, Hkv,
+                                                  _int32(Lk, "Lk"), d)
 
 
 def attn_fwd_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, cu_seqlens_q, max_seqlen_q,
@@ -593,6 +610,8 @@ def attn_fwd_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq
                          causal, window_left, window_right)
         if got is not None:
             return got
+    max_seqlen_q = _int32(max_seqlen_q, "max_seqlen_q")
+    window_left, window_right = _window(window_left), _window(window_right)
     dev = _first(q, _BF16, 3, "q")
     total_q, Hq, d = q.shape
     num_pages, page_size, Hkv, dk = _cache_shape(k_pages, v_pages, k_scales, v_scales, dev)

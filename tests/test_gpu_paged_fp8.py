@@ -643,6 +643,30 @@ def test_buffers_given(fl):
             fl.attn_paged_plan(held, _i32(new), free, t2, page, 50, **bad)
 
 
+def test_arguments_beyond_32_bits(fl):
+    """A window wider than 32 bits hold is no window; a size of that kind is refused."""
+    g = torch.Generator().manual_seed(28)
+    cache = [t.cuda() for t in _cache(8, 16, 2, 128, g)]
+    table, lens = _i32([list(range(8))]), _i32([128])
+    for new in (1, 5, 40):
+        q = torch.randn(new, 4, 128, generator=g).to(torch.bfloat16).cuda()
+        args = (q, *cache, table, lens, _i32([0, new]))
+        want = fl.attn_fwd_paged_fp8(*args, new)
+        for w in (2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 3, 2 ** 63 - 1):
+            got = fl.attn_fwd_paged_fp8(*args, new, window_left=w, window_right=w)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+            if new == 1:
+                got = fl.attn_decode_paged_fp8(q[:, :, None], *cache, table, lens, window_left=w)
+                assert torch.equal(got[0][:, :, 0], want[0]) and torch.equal(got[1].T, want[1])
+        with pytest.raises(ValueError, match="max_seqlen_q"):
+            fl.attn_fwd_paged_fp8(*args, 2 ** 32 + new)
+    with pytest.raises(ValueError, match="num_splits"):
+        fl.attn_decode_paged_fp8(q[:1, :, None], *cache, table, lens, num_splits=2 ** 32 + 1)
+    for kw, match in ((dict(page_size=2 ** 32 + 16, max_tokens=4), "page_size"), (dict(page_size=16, max_tokens=2 ** 32 + 4), "max_tokens")):
+        with pytest.raises(ValueError, match=match):
+            fl.attn_paged_plan(lens, lens, _i32([1]), table.clone(), **kw)
+
+
 def test_window_over_a_long_table(fl):
     """The library splits what the window leaves, whoever brings the buffers: the same bits."""
     g = torch.Generator().manual_seed(27)

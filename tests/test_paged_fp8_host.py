@@ -112,6 +112,24 @@ def test_fwd_argument_checks(fl):
     assert _attend(fl, "fwd", B=1, T=3, most=3, width=256, bytes=need - 1) == fl.FATTN_ERR_WORKSPACE
 
 
+def test_integers_beyond_32_bits(fl):
+    """Refused where they are sizes; a window of that length is as wide as any."""
+    for x in (2 ** 31, 2 ** 32 + 1, -2 ** 31 - 1, 10 ** 30):
+        with pytest.raises(ValueError, match="max_tokens"):
+            fl._int32(x, "max_tokens")
+    assert [fl._int32(x, "") for x in (0, -5, 2 ** 31 - 1, -2 ** 31)] == [0, -5, 2 ** 31 - 1, -2 ** 31]
+    for x in (1.0, "3", None):
+        with pytest.raises(TypeError):
+            fl._int32(x, "max_tokens")
+        with pytest.raises(TypeError):
+            fl._window(x)
+    assert [fl._window(x) for x in (-1, -2 ** 40, 0, 7, 2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 63 + 5)] == [-1, -1, 0, 7] + [2 ** 31 - 1] * 4
+    with pytest.raises(ValueError):
+        fl.attn_fwd_paged_fp8_workspace_bytes(1, 2 ** 32 + 8, 8, 8, 8, 64, 128)
+    with pytest.raises(ValueError):
+        fl.attn_decode_paged_fp8_auto_splits(1, 8, 8, 2 ** 32 + 64, 128)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_more_keys_never_mean_fewer_splits(fl, d):
     """A workspace sized for the whole table serves every window of it."""
