@@ -5,16 +5,18 @@ the native part of its Python binding, with g++ against the installed torch.
 
 The shared library links the CUDA runtime statically and resolves the
 driver's tensor-map encoder at run time, so it loads on a machine without a
-GPU (every entry point then reports FATTN_ERR_NO_DEVICE).
+GPU (every entry point then reports FATTN_ERR_NO_DEVICE).  It needs neither
+torch nor Python and is built first; where the native part of the binding cannot
+be built (no torch, no headers of it or of Python), a warning says why.
 """
 from __future__ import annotations
 
-import importlib.util
 import os
 import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -45,7 +47,11 @@ def build_calls(force: bool = False) -> str:
     """The binding's native calls (no CUDA code: any host compiler)."""
     if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= os.path.getmtime(CALLS_SRC):
         return CALLS
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    try:
+        import torch
+    except ImportError as e:
+        raise RuntimeError(f"torch does not import ({e})") from e
+    torch_dir = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     tmp = CALLS + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared"]
@@ -61,7 +67,15 @@ def build_calls(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    build_calls(force)
+    build_lib(force, verbose)
+    try:
+        build_calls(force)
+    except (RuntimeError, OSError) as e:
+        warnings.warn(f"the native calls of the Python binding are not built: {e}")
+    return LIB
+
+
+def build_lib(force: bool = False, verbose: bool = False) -> str:
     if not force and not needs_build():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"

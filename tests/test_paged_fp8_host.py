@@ -2,6 +2,7 @@
 call, workspace sizes, and the plain implementations the GPU tests use against
 closed forms."""
 import math
+import sys
 
 import pytest
 import torch
@@ -15,6 +16,17 @@ def fl():
     build.build()
     from io_aware_exact_34_b200 import fattn
     return fattn
+
+
+def test_library_builds_without_torch(fl, monkeypatch):
+    from io_aware_exact_34_b200 import build
+    built = []
+    monkeypatch.setattr(build, "build_lib", lambda force, verbose: built.append(force) or build.LIB)
+    monkeypatch.setitem(sys.modules, "torch", None)  # import torch raises ImportError
+    with pytest.raises(RuntimeError, match="torch does not import"):
+        build.build_calls(force=True)
+    with pytest.warns(UserWarning, match="torch does not import"):
+        assert build.build(force=True) == build.LIB and built == [True]
 
 
 A = [0x100000 * (i + 1) for i in range(12)]  # never dereferenced: every call below fails validation first
