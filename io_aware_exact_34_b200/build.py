@@ -1,4 +1,4 @@
-"""Build ``libfattn.so`` in-tree with nvcc for sm_100a, and ``_fattn_calls.so``,
+"""Build ``libfattn.so`` in-tree with nvcc for sm_100a, and ``_fattn_calls.*.so``,
 the native part of its Python binding, with g++ against the installed torch.
 
     python -m io_aware_exact_34_b200.build [--verbose]
@@ -6,8 +6,9 @@ the native part of its Python binding, with g++ against the installed torch.
 The shared library links the CUDA runtime statically and resolves the
 driver's tensor-map encoder at run time, so it loads on a machine without a
 GPU (every entry point then reports FATTN_ERR_NO_DEVICE).  It needs neither
-torch nor Python and is built first; where the native part of the binding cannot
-be built (no torch, no headers of it or of Python), a warning says why.
+torch nor Python; where the native part of the binding cannot be built (no
+torch, no headers of it or of Python), a warning says why and the binding goes
+without it.
 """
 from __future__ import annotations
 
@@ -18,6 +19,8 @@ import sys
 import sysconfig
 import warnings
 
+from . import calls_path
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "fattn_api.cu")
@@ -26,7 +29,6 @@ LIB = os.path.join(PKG, "libfattn.so")
 DEPS = [os.path.join(PKG, "csrc", f) for f in os.listdir(os.path.join(PKG, "csrc")) if f.endswith((".cu", ".cuh"))] + [
     os.path.join(INCLUDE, "fattn.h")]
 CALLS_SRC = os.path.join(PKG, "csrc", "binding.cpp")
-CALLS = os.path.join(PKG, "_fattn_calls.so")
 
 
 def _nvcc() -> str:
@@ -44,16 +46,17 @@ def needs_build() -> bool:
 
 
 def build_calls(force: bool = False) -> str:
-    """The binding's native calls (no CUDA code: any host compiler)."""
-    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= os.path.getmtime(CALLS_SRC):
-        return CALLS
+    """The binding's native calls (no CUDA code: any host compiler), for the installed torch."""
     try:
         import torch
     except ImportError as e:
         raise RuntimeError(f"torch does not import ({e})") from e
+    out = calls_path(torch.__version__)
+    if not force and os.path.exists(out) and os.path.getmtime(out) >= os.path.getmtime(CALLS_SRC):
+        return out
     torch_dir = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
-    tmp = CALLS + f".tmp{os.getpid()}"
+    tmp = out + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared"]
     for d in (os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
               sysconfig.get_paths()["include"], os.path.join(cuda, "include")):
@@ -62,8 +65,8 @@ def build_calls(force: bool = False) -> str:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("g++ failed:\n" + res.stdout + res.stderr)
-    os.replace(tmp, CALLS)
-    return CALLS
+    os.replace(tmp, out)
+    return out
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -71,7 +74,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     try:
         build_calls(force)
     except (RuntimeError, OSError) as e:
-        warnings.warn(f"the native calls of the Python binding are not built: {e}")
+        warnings.warn(f"the native calls of the Python binding are not built, it goes without them: {e}")
     return LIB
 
 

@@ -6,8 +6,9 @@
 // function here returns None whenever anything is not as the ordinary call has
 // it (a wrong type or shape, a tensor elsewhere, an optional buffer given, an
 // error status): the caller then takes the Python path, which makes every
-// check again and raises with a message.  Nothing has been enqueued by then: a
-// call that the library refuses enqueues nothing.
+// check again and raises with a message.  A call that the library refuses has
+// enqueued nothing by then; one whose launch fails is made again, over the
+// same outputs, and its second failure is the one that is raised.
 //
 // The library's functions are handed over as addresses, so this module links
 // against nothing but torch.

@@ -12,8 +12,11 @@ import ctypes
 import importlib.util
 import operator
 import os
+import warnings
 
 import torch
+
+from . import calls_path
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfattn.so")
 if not os.path.exists(_LIB_PATH):
@@ -399,16 +402,27 @@ def attn_decode_paged(q, k_pages, v_pages, block_table, seqlens_k, o=None, lse=N
 # The calls of a serving step are short (a few us on the GPU).  Their ordinary
 # case runs in native code (csrc/binding.cpp: the same checks and allocations,
 # then the same library call); it answers None to anything else, which then goes
-# through the checks below and gets their messages.
-if not os.path.exists(os.path.join(os.path.dirname(_LIB_PATH), "_fattn_calls.so")):
-    raise ImportError("_fattn_calls.so is not built; run `python -m io_aware_exact_34_b200.build`")
-_calls_spec = importlib.util.spec_from_file_location(
-    "io_aware_exact_34_b200._fattn_calls", os.path.join(os.path.dirname(_LIB_PATH), "_fattn_calls.so"))
-_calls = importlib.util.module_from_spec(_calls_spec)
-_calls_spec.loader.exec_module(_calls)
-for _name in ("attn_paged_plan", "attn_append_paged_fp8", "attn_decode_paged_fp8", "attn_decode_paged_fp8_auto_splits",
-              "attn_fwd_paged_fp8", "attn_fwd_paged_fp8_workspace_bytes"):
-    _calls.bind(_name, ctypes.cast(getattr(lib, _name), ctypes.c_void_p).value)
+# through the checks below and gets their messages.  The module is built against
+# one torch and loaded with that one only; without it every call takes the checks
+# below, with the same results some 10 us later.
+def _load_calls(path):
+    """The native module at ``path``, bound to the library's functions, or None where there is none that loads."""
+    if not os.path.exists(path):
+        return None
+    spec = importlib.util.spec_from_file_location("io_aware_exact_34_b200._fattn_calls", path)
+    try:
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except ImportError as e:
+        warnings.warn(f"{path} does not load ({e}); the paged-cache calls go without it")
+        return None
+    for name in ("attn_paged_plan", "attn_append_paged_fp8", "attn_decode_paged_fp8", "attn_decode_paged_fp8_auto_splits",
+                 "attn_fwd_paged_fp8", "attn_fwd_paged_fp8_workspace_bytes"):
+        module.bind(name, ctypes.cast(getattr(lib, name), ctypes.c_void_p).value)
+    return module
+
+
+_calls = _load_calls(calls_path(torch.__version__))
 _BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
 
 
@@ -429,7 +443,7 @@ def _first(t, dtype, ndim, name):
     return index
 
 
-_stream_of = torch._C._cuda_getCurrentRawStream  # device index -> cudaStream_t
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # device index -> cudaStream_t (torch without CUDA: none)
 
 
 def _int32(x, name):
@@ -454,7 +468,7 @@ def attn_paged_plan(seqlens_k, seqlens_new, free_pages, block_table, page_size, 
     cu_seqlens int32 [B + 1], seqlens_out int32 [B], counts int32 [2]: tokens,
     pages needed).  Tokens without a page and places behind the last token have
     slot -1."""
-    if slot_map is None and cu_seqlens is None and seqlens_out is None and counts is None:
+    if _calls is not None and slot_map is None and cu_seqlens is None and seqlens_out is None and counts is None:
         got = _calls.plan(seqlens_k, seqlens_new, free_pages, block_table, page_size, max_tokens)
         if got is not None:
             return got
@@ -529,7 +543,7 @@ def attn_append_paged_fp8(k, v, slot_map, k_pages, v_pages, k_scales, v_scales):
     tokens of a longer map are taken as a slice); k_pages, v_pages: uint8 e4m3
     codes [num_pages, page_size, Hkv, d]; k_scales, v_scales: fp32
     [num_pages, Hkv]."""
-    if _calls.append(k, v, slot_map, k_pages, v_pages, k_scales, v_scales):
+    if _calls is not None and _calls.append(k, v, slot_map, k_pages, v_pages, k_scales, v_scales):
         return
     dev = _first(slot_map, _I64, 1, "slot_map")
     num_pages, page_size, H, d = _cache_shape(k_pages, v_pages, k_scales, v_scales, dev)
@@ -556,7 +570,7 @@ def attn_decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, 
     """Split-KV decode over a paged 8-bit cache.  q: bf16 [B,Hq,1,d]; cache as
     attn_append_paged_fp8; block_table: int32 [B, max_pages]; seqlens_k: int32
     [B], the new token included -> (o [B,Hq,1,d], lse [B,Hq])."""
-    if o is None and lse is None and workspace is None:
+    if _calls is not None and o is None and lse is None and workspace is None:
         got = _calls.decode(q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, scale, window_left, num_splits)
         if got is not None:
             return got
@@ -605,7 +619,7 @@ def attn_fwd_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq
     new tokens of all sequences; cu_seqlens_q: int32 [B + 1]; seqlens_k: int32
     [B], the new tokens included; cache and block_table as
     attn_decode_paged_fp8 -> (o [total_q, Hq, d], lse [Hq, total_q])."""
-    if o is None and lse is None and workspace is None:
+    if _calls is not None and o is None and lse is None and workspace is None:
         got = _calls.fwd(q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, cu_seqlens_q, max_seqlen_q, scale,
                          causal, window_left, window_right)
         if got is not None:

@@ -727,6 +727,28 @@ def test_serving_run(fl):
     _serve(fl, [[200, 1, 90], [1, 1, 1], [130, 3, 0]], 64, 4, 4, 64, seed=32)
 
 
+def test_without_native_calls(fl, monkeypatch):
+    """The interpreted path of the four calls: the same bits."""
+    g = torch.Generator().manual_seed(43)
+    pages, page, hq, hkv, d = 20, 16, 8, 2, 128
+    start = [t.cuda() for t in _cache(pages, page, hkv, d, g)]
+    kv = torch.randn(70, 2, hkv, d, generator=g).to(torch.bfloat16).cuda()
+    q = torch.randn(70, hq, d, generator=g).to(torch.bfloat16).cuda()
+
+    def run():
+        cache, table = [t.clone() for t in start], _i32([[0, 1] + [-1] * 6, [2] + [-1] * 7])
+        plan = fl.attn_paged_plan(_i32([31, 16]), _i32([66, 4]), _i32(list(range(3, 20))), table, page, 70)
+        fl.attn_append_paged_fp8(kv[:, 0], kv[:, 1], plan[0], *cache)
+        return [*plan, table, *cache, *fl.attn_decode_paged_fp8(q[:2, :, None], *cache, table, plan[2]),
+                *fl.attn_fwd_paged_fp8(q, *cache, table, plan[2], plan[1], 66, causal=True, window_left=50)]
+
+    native = run()
+    assert fl._calls is not None
+    monkeypatch.setattr(fl, "_calls", None)
+    for a, b in zip(native, run()):
+        assert torch.equal(a, b)
+
+
 def test_captured_step(fl):
     """Plan, append and decode in one CUDA graph: replays take the lengths and rows that the buffers hold then."""
     g = torch.Generator().manual_seed(41)

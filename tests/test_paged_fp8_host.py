@@ -2,6 +2,9 @@
 call, workspace sizes, and the plain implementations the GPU tests use against
 closed forms."""
 import math
+import os
+import shutil
+import subprocess
 import sys
 
 import pytest
@@ -16,6 +19,38 @@ def fl():
     build.build()
     from io_aware_exact_34_b200 import fattn
     return fattn
+
+
+def test_native_calls_are_loaded(fl):
+    """Where they can be built they are, and they are the ones in use."""
+    from io_aware_exact_34_b200 import build, calls_path
+    assert build.build_calls() == calls_path(torch.__version__) == fl._calls.__file__
+    assert torch.__version__ in os.path.basename(fl._calls.__file__)
+
+
+def test_native_calls_that_do_not_load(fl, tmp_path):
+    """No file, or one that is no module: the binding goes without."""
+    assert fl._load_calls(str(tmp_path / "none.so")) is None
+    broken = tmp_path / "broken.so"
+    broken.write_bytes(b"no shared object")
+    with pytest.warns(UserWarning, match="broken.so does not load"):
+        assert fl._load_calls(str(broken)) is None
+
+
+def test_binding_imports_without_native_calls(fl, tmp_path):
+    """The package with its library alone (another torch's native calls beside it are not touched)."""
+    from io_aware_exact_34_b200 import build
+    pkg = tmp_path / "io_aware_exact_34_b200"
+    pkg.mkdir()
+    for f in os.listdir(build.PKG):
+        if f.endswith(".py"):
+            shutil.copy(os.path.join(build.PKG, f), pkg)
+    os.symlink(build.LIB, pkg / "libfattn.so")
+    for f in ("_fattn_calls.so", "_fattn_calls.torch-0.0.so"):
+        (pkg / f).write_bytes(b"no shared object")
+    code = "from io_aware_exact_34_b200 import fattn; print(fattn._calls, fattn.attn_decode_paged_fp8_auto_splits(1, 8, 8, 64, 128))"
+    res = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True)
+    assert res.returncode == 0 and res.stdout.split() == ["None", "1"], res.stderr
 
 
 def test_library_builds_without_torch(fl, monkeypatch):
