@@ -1,6 +1,7 @@
 """The paged 8-bit KV cache on the GPU (plan, append, decode, multi-token
 attention) against the plain 64-bit implementations of tests/_paged_ref.py."""
 import math
+import threading
 
 import pytest
 import torch
@@ -682,6 +683,37 @@ def test_window_over_a_long_table(fl):
         assert torch.equal(a[0], o) and torch.equal(a[1], lse)
 
 
+@pytest.mark.parametrize("new,left", [(1, -1), (1, 900), (6, -1), (512, -1), (512, 300)])
+def test_table_as_wide_as_a_context(fl, new, left):
+    """A table of 131072 keys over short sequences, anything in its unused entries: splits and parts by the table's
+    width, most of them empty, and the same answers."""
+    g = torch.Generator().manual_seed(29)
+    page, hq, hkv, d, lens = 16, 8, 2, 128, [3000, 520, 37]
+    width, pages = 131072 // page, sum(-(-x // page) for x in lens) + 2
+    adds = [min(new, x) for x in lens]
+    table = _table(lens, page, 200, pages, g)
+    wide = torch.randint(-2 ** 31, 2 ** 31, (len(lens), width), generator=g, dtype=torch.int64).int()
+    for b, n in enumerate(lens):
+        held = -(-n // page)
+        wide[b, :held] = torch.tensor(table[b][:held])
+    cache = _cache(pages, page, hkv, d, g)
+    q = torch.randn(sum(adds), hq, d, generator=g).to(torch.bfloat16)
+    cu = [0] + torch.tensor(adds).cumsum(0).tolist()
+    dev = [t.cuda() for t in cache]
+    if new == 1:
+        o, lse = fl.attn_decode_paged_fp8(q[:, :, None].cuda(), *dev, wide.cuda(), _i32(lens), window_left=left)
+        o = o[:, :, 0]
+    else:
+        o, lse = fl.attn_fwd_paged_fp8(q.cuda(), *dev, wide.cuda(), _i32(lens), _i32(cu), max(adds), causal=True, window_left=left)
+        lse = lse.T
+    for b, n in enumerate(lens):
+        k, v = [ref.gather(ref.value(cache[i]), cache[2 + i].double(), table[b], n) for i in range(2)]
+        for i in sorted({0, adds[b] // 2, adds[b] - 1}):
+            seen = n - adds[b] + i + 1
+            exp = ref.attention(q[cu[b] + i][None].double(), k[:seen], v[:seen], float(torch.tensor(d ** -0.5, dtype=torch.float32)), left=left)
+            _check_rows(o[cu[b] + i][None], lse[cu[b] + i][None], exp, d, seen, f"sequence {b}, token {i}")
+
+
 # ---------------------------------------------------------------- as they are used
 def _serve(fl, steps, page, hq, hkv, d, seed):
     """A prompt batch, then decode steps, then drafted tokens: every step plans, appends and attends."""
@@ -798,6 +830,72 @@ def test_captured_step(fl):
         lens.copy_(want[2])
         n = int(want[3][1])
         free[:free.numel() - n] = free[n:].clone()
+
+
+def test_captured_parts(fl):
+    """Splits and parts that merge through memory, captured; two graphs that share the workspaces, replayed in turn over
+    new lengths and queries."""
+    g = torch.Generator().manual_seed(44)
+    page, hq, hkv, d, width = 16, 8, 2, 128, 400
+    table = _i32([torch.randperm(500, generator=g)[:width].tolist()])
+    cache = [t.cuda() for t in _cache(500, page, hkv, d, g)]
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+
+    def made(new):
+        st = dict(q=torch.randn(new, hq, d, generator=g).to(torch.bfloat16).cuda(), lens=_i32([6000]), cu=_i32([0, new]))
+        st["o"], st["lse"] = torch.empty_like(st["q"]), torch.empty(hq, new, device="cuda")
+        st["do"], st["dlse"] = torch.empty(1, hq, 1, d, dtype=torch.bfloat16, device="cuda"), torch.empty(1, hq, device="cuda")
+        return st
+
+    def run(st, **kw):
+        a = fl.attn_fwd_paged_fp8(st["q"], *cache, table, st["lens"], st["cu"], len(st["q"]), causal=True, **kw)
+        kw.update({k: st["d" + k] for k in ("o", "lse") if k in kw})
+        return [*a, *fl.attn_decode_paged_fp8(st["q"][:1, :, None], *cache, table, st["lens"], num_splits=12, **kw)]
+
+    states = [made(70), made(5)]
+    graphs = []
+    for st in states:
+        run(st)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            run(st, o=st["o"], lse=st["lse"], workspace=ws)
+    for step in range(6):
+        st = states[step % 2]
+        st["lens"].fill_(6400 - 900 * step)
+        st["q"].copy_(torch.randn(st["q"].shape, generator=g))
+        graphs[step % 2].replay()
+        for a, b in zip((st["o"], st["lse"], st["do"], st["dlse"]), run(st)):
+            assert torch.equal(a, b), step
+
+
+def test_host_threads(fl):
+    """Calls from several host threads, each on a stream of its own."""
+    g = torch.Generator().manual_seed(45)
+    lens, page = [3000, 2500], 16
+    pages = sum(-(-x // page) for x in lens)
+    table, held = _i32(_table(lens, page, 190, pages, g)), _i32(lens)
+    cache = [t.cuda() for t in _cache(pages, page, 2, 128, g)]
+    qs = [torch.randn(120, 8, 128, generator=g).to(torch.bfloat16).cuda() for _ in range(4)]
+    cu = _i32([0, 60, 120])
+    want = [fl.attn_fwd_paged_fp8(q, *cache, table, held, cu, 60, causal=True) for q in qs]
+    torch.cuda.synchronize()
+    got = [None] * 4
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for turn in range(10):
+                got[i] = fl.attn_fwd_paged_fp8(qs[i], *cache, table, held, cu, 60, causal=True,
+                                               workspace=None if turn % 2 else torch.empty(8 << 20, dtype=torch.uint8, device="cuda"))
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for a, b in zip(got, want):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
 def test_other_stream(fl):
