@@ -322,8 +322,11 @@ size_t attn_decode_workspace_bytes(int B, int H, int Lk, int d, int num_splits);
  *   k_pages, v_pages    device, e4m3 codes [num_pages, page_size, Hkv, d]
  *                       (token-major pages, as attn_decode_paged); d 64 or 128,
  *                       16-byte aligned; num_pages * page_size <= 2^40
- *   k_scales, v_scales  device, fp32 [num_pages, Hkv], finite and > 0: code c of
- *                       page p and head h stands for e4m3(c) * scales[p, h]
+ *   k_scales, v_scales  device, fp32 [num_pages, Hkv], finite and > 0 for the
+ *                       pages in use: code c of page p and head h stands for
+ *                       e4m3(c) * scales[p, h].  With another scale the rows that
+ *                       see the page get unspecified values, and not always NaN
+ *                       (a long run counts a NaN or negative K scale as 1e-37)
  *   page_size           a power of two >= 16
  *   block_table         device, int32 [B, max_pages]: logical page i of sequence
  *                       b is physical page block_table[b*max_pages + i]; the
@@ -344,7 +347,8 @@ size_t attn_decode_workspace_bytes(int B, int H, int Lk, int d, int num_splits);
  *   free_pages   device, int32 [num_free], physical pages not in use (may be
  *                NULL when num_free = 0); only read
  *   block_table  device, int32 [B, max_pages]: the entries of the pages taken
- *                are written, all others are left as they were
+ *                are written (of those with a token among the first
+ *                max_tokens), all others are left as they were
  *   slot_map     device, int64 [max_tokens] (written): the slot of every token
  *                of the packed batch, sequence after sequence; -1 for the
  *                places behind the last token, and for a token that has no page
@@ -356,7 +360,8 @@ size_t attn_decode_workspace_bytes(int B, int H, int Lk, int d, int num_splits);
  *                overlapping the inputs
  *   counts       device, int32 [2] (written): tokens of the batch, and pages it
  *                needs.  counts[0] > max_tokens or counts[1] > num_free says that
- *                some tokens have no slot; the next free list is
+ *                some tokens have no slot and their pages no entry, while
+ *                seqlens_out counts them; otherwise the next free list is
  *                free_pages + counts[1].
  * B <= 16384.  One kernel; sums beyond 2^31 - 1 are written as 2^31 - 1.
  * Everything is read on the device, so a captured graph takes new lengths (up
@@ -417,7 +422,10 @@ int attn_append_paged_fp8(const void* k, const void* v, long long k_stride, long
  *   num_splits   splits of a sequence's attended keys at most (evenly, by the
  *                sequence's own length, at least 256 keys to a split), or 0 for
  *                attn_decode_paged_fp8_auto_splits(B, Hq, Hkv, max_pages*page_size, d)
- *                (with a window of fewer keys: as many as for those keys, never more)
+ *                (with a window of fewer keys: as many as for those keys, never more).
+ *                That choice takes the table's width for the lengths: a table much
+ *                wider than the sequences costs 5-10 %, never another result but
+ *                for the order of sums
  *   workspace    device scratch of attn_decode_workspace_bytes(B, Hq, Lk, d, S)
  *                bytes for S splits, 16-byte aligned; not needed (may be NULL)
  *                when S = 1; contents ignored on entry, unspecified on return
@@ -460,7 +468,10 @@ int attn_decode_paged_fp8_auto_splits(int B, int Hq, int Hkv, int Lk, int d);
  *   causal, window_left, window_right: the mask of attn_fwd per sequence
  *                 (bottom-right aligned: the last query sits at the last key)
  *   workspace     device scratch of attn_fwd_paged_fp8_workspace_bytes bytes,
- *                 32-byte aligned (may be NULL when that is 0)
+ *                 32-byte aligned (may be NULL when that is 0); in long runs it
+ *                 holds the parts of at most 147 pairs of row tiles, whatever
+ *                 the batch is.  A table of max_pages far beyond the lengths
+ *                 costs time (empty parts), as in decode
  * Offsets and lengths are clamped so that no access leaves the tensors.
  * Precision and key rows outside the mask as attn_decode_paged_fp8, but for
  * the query rows of sequences with max_seqlen_q * Hq / Hkv > 48: they enter the

@@ -51,9 +51,9 @@
 // 4097 keys: 9.6 us in 8 splits, 11.2 through the workspace, 10.6 in 16 splits).
 // Longer work goes through the workspace and a merge kernel that starts by
 // programmatic launch: there the heads of one key range stand next to each
-// other in the grid and read the same DRAM pages together (32 x 32768 keys: 320
-// us, 370-390 with the splits of a head, or one split of all sequences, next to
-// each other).
+// other in the grid and read the same DRAM pages together (32 x 32768 keys: 345
+// us a call, 360-390 with the splits of a head, or one split of all sequences,
+// next to each other).
 #pragma once
 
 #include <cuda_bf16.h>

@@ -467,7 +467,8 @@ def attn_paged_plan(seqlens_k, seqlens_new, free_pages, block_table, page_size, 
     updated in place with the pages taken -> (slot_map int64 [max_tokens],
     cu_seqlens int32 [B + 1], seqlens_out int32 [B], counts int32 [2]: tokens,
     pages needed).  Tokens without a page and places behind the last token have
-    slot -1."""
+    slot -1.  cu_seqlens, seqlens_out and counts may be parts of one allocation,
+    which lives as long as any of them."""
     if _calls is not None and slot_map is None and cu_seqlens is None and seqlens_out is None and counts is None:
         got = _calls.plan(seqlens_k, seqlens_new, free_pages, block_table, page_size, max_tokens)
         if got is not None:
